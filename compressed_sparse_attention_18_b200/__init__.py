@@ -24,7 +24,8 @@ ENTRY_POINTS = ("csa_status_string", "csa_version", "csa_last_cuda_error", "csa_
                 "csa_index_topk_workspace_size", "csa_index_topk", "csa_index_scores", "csa_topk_workspace_size",
                 "csa_topk", "csa_attn_workspace_size", "csa_sparse_attn", "hca_dense_attn",
                 "csa_index_topk_noalloc", "csa_device_status", "csa_check_error_path",
-                "csa_pack_fp8_window", "csa_attn_kernel_count")
+                "csa_pack_fp8_window", "csa_attn_kernel_count", "csa_quant_fp8", "csa_gemm_fp8", "csa_unpack_fp4",
+                "csa_unpack_fp8_window")
 # (PagedCache: a paged pool + block table, accepted wherever a PackedCache is)
 
 _u32, _i32, _f32, _vp = ctypes.c_uint32, ctypes.c_int32, ctypes.c_float, ctypes.c_void_p
@@ -77,6 +78,22 @@ class Fp8WindowArgs(ctypes.Structure):
                 ("src", _vp), ("row0", _vp), ("codes", _vp), ("scales", _vp), ("rope", _vp)]
 
 
+class QuantFp8Args(ctypes.Structure):
+    _fields_ = [("struct_size", _u32), ("rows", _i32), ("K", _i32), ("block_rows", _i32), ("src", _vp),
+                ("codes", _vp), ("scales", _vp)]
+
+
+class GemmFp8Args(ctypes.Structure):
+    _fields_ = [("struct_size", _u32), ("M", _i32), ("N", _i32), ("K", _i32), ("x", _vp), ("x_scales", _vp),
+                ("W", _vp * 2), ("W_scales", _vp * 2), ("out", _vp * 2)]
+
+
+class UnpackArgs(ctypes.Structure):
+    _fields_ = [("struct_size", _u32), ("B", _i32), ("n", _i32), ("d", _i32), ("d_rope", _i32), ("n_max", _i32),
+                ("global_scale", _f32), ("codes", _vp), ("scales", _vp), ("rope", _vp), ("row0", _vp), ("idx", _vp),
+                ("out", _vp), ("pages", PageMap)]
+
+
 _lib.csa_status_string.restype = ctypes.c_char_p
 _lib.csa_status_string.argtypes = [ctypes.c_int]
 _lib.csa_version.restype = ctypes.c_int
@@ -85,7 +102,9 @@ _lib.csa_device_status.restype = ctypes.c_int
 _lib.csa_device_status.argtypes = [_vp]
 _lib.csa_check_error_path.restype = ctypes.c_int
 _lib.csa_check_error_path.argtypes = [_u32, _vp]
-for _name, _st in (("csa_compress", CompressArgs), ("csa_pack_fp4", PackArgs), ("csa_pack_fp8_window", Fp8WindowArgs)):
+for _name, _st in (("csa_compress", CompressArgs), ("csa_pack_fp4", PackArgs), ("csa_pack_fp8_window", Fp8WindowArgs),
+                   ("csa_quant_fp8", QuantFp8Args), ("csa_gemm_fp8", GemmFp8Args), ("csa_unpack_fp4", UnpackArgs),
+                   ("csa_unpack_fp8_window", UnpackArgs)):
     getattr(_lib, _name).restype = ctypes.c_int
     getattr(_lib, _name).argtypes = [ctypes.POINTER(_st), _vp]
 _lib.csa_index_topk_workspace_size.restype = ctypes.c_size_t
@@ -159,6 +178,35 @@ def _ws(nbytes: int, device, ws=None, zero=False):
     return (torch.zeros if zero else torch.empty)(nbytes, dtype=torch.uint8, device=device)
 
 
+def _need(t, what, dtype, shape=None, like=None):
+    """Check one tensor argument of a call: its type, its shape (None: any size) and that it is on `like`'s device."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+        raise CSAError(f"{what}: a {dtype} tensor is needed")
+    if shape is not None and (t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape))):
+        raise CSAError(f"{what}: shape {tuple(t.shape)}, expected {tuple('any' if w is None else w for w in shape)}")
+    if like is not None and t.device != like.device:
+        raise CSAError(f"{what}: on {t.device}, the other operands are on {like.device}")
+
+
+class _On:
+    """The device and stream of a call: what it allocates belongs to that stream, its kernels launch on the
+    operands' device whichever device is current."""
+
+    def __init__(self, t, stream):
+        _ptr(t)                                          # a CUDA tensor
+        if stream is not None and stream.device != t.device:
+            raise CSAError(f"the stream is on {stream.device}, the operands are on {t.device}")
+        self.stream = stream if stream is not None else torch.cuda.current_stream(t.device)
+        self._ctx = torch.cuda.stream(self.stream)       # also makes its device current
+
+    def __enter__(self):
+        self._ctx.__enter__()
+        return self.stream
+
+    def __exit__(self, *exc):
+        return self._ctx.__exit__(*exc)
+
+
 # ------------------------------------------------------------------------------------------- API
 
 def _page_map(cache):
@@ -196,8 +244,12 @@ def _fp4_target(cache, row0):
 def compress(*, b_pos, ratio, d_rope=0, rope_theta=0.0, pos0=None, x=None, W_kv=None, W_g=None, C=None, Z=None,
              W_IK=None, c_out=None, kI_out=None, kv_cache=None, ki_cache=None, row0=None, stream=None):
     """Compressor.  Projection mode (x [B,T,d_m], W_kv/W_g [d_m,d]) fills C, Z [B,T,d]; pooling mode
-    reads C, Z.  kv_cache / ki_cache (PackedCache, rows row0[b] + i) also receive the FP4-packed entries
+    reads C, Z.  With FP8 weights (W_kv and W_g Fp8Blocks [d, d_m], block_rows 128) the projections run in FP8: x is
+    quantised by quant_fp8 (or given as Fp8Blocks, with B = 1) and gemm_fp8 fills C and Z.  kv_cache / ki_cache (PackedCache, rows row0[b] + i) also receive the FP4-packed entries
     and indexer keys from the same launch.  Returns (c [B,T//r,d], k_I [B,T//r,d_I] or None, C, Z)."""
+    if isinstance(W_kv, Fp8Blocks) or isinstance(W_g, Fp8Blocks) or isinstance(x, Fp8Blocks):
+        C, Z = _project_fp8(x, W_kv, W_g, C, Z, stream)
+        x = W_kv = W_g = None
     if x is not None:
         B, T, dm = x.shape
         d = W_kv.shape[1]
@@ -424,3 +476,133 @@ def attn_kernel_count(q, q_pos, cache, n_c, idx, win_kv, win_pos0, *, ratio, win
     a.flags = (CSA_EARLY_START if early_start else 0) | (CSA_CLUSTER_MERGE if cluster else 0)
     a.out_rope_theta = out_rope_theta
     return _lib.csa_attn_kernel_count(ctypes.byref(a), 1 if hca else 0)
+
+
+# ---------------------------------------------------------------------------------- FP8 projections
+
+class Fp8Blocks:
+    """A bf16 matrix quantised by quant_fp8: codes [rows, K] u8 (E4M3) and fp32 scales
+    [ceil(rows / block_rows), ceil(K / 128)], block_rows 1 (activations) or 128 (weights)."""
+
+    def __init__(self, codes, scales, block_rows):
+        if block_rows not in (1, 128):
+            raise CSAError("Fp8Blocks: block_rows is 1 or 128")
+        _need(codes, "Fp8Blocks codes", torch.uint8, (None, None))
+        rows, K = codes.shape
+        _need(scales, "Fp8Blocks scales", torch.float32, (-(-rows // block_rows), -(-K // 128)), codes)
+        self.codes, self.scales, self.block_rows = codes, scales, block_rows
+
+    @property
+    def shape(self):
+        return tuple(self.codes.shape)
+
+
+def quant_fp8(src, *, block_rows=1, out=None, stream=None):
+    """Quantise src [..., K] bf16 to E4M3 with one fp32 scale per 128 channels of a row (block_rows = 1) or per
+    128 x 128 block (block_rows = 128).  Leading dimensions are rows.  Returns Fp8Blocks (out, if given)."""
+    _need(src, "quant_fp8 src", torch.bfloat16)
+    if src.dim() < 1 or src.shape[-1] < 1:
+        raise CSAError("quant_fp8 src: [..., K] with K >= 1 is needed")
+    K = src.shape[-1]
+    rows = src.numel() // K
+    with _On(src, stream) as st:
+        if out is None:
+            out = Fp8Blocks(torch.empty((rows, K), dtype=torch.uint8, device=src.device),
+                            torch.empty((-(-rows // block_rows) if block_rows > 0 else 0, -(-K // 128)),
+                                        dtype=torch.float32, device=src.device), block_rows)
+        elif out.shape != (rows, K) or out.block_rows != block_rows or out.codes.device != src.device:
+            raise CSAError(f"quant_fp8 out: {out.shape} with block_rows {out.block_rows} on {out.codes.device}, "
+                           f"expected {(rows, K)} with block_rows {block_rows} on {src.device}")
+        a = QuantFp8Args(ctypes.sizeof(QuantFp8Args), rows, K, block_rows, _ptr(src), _ptr(out.codes),
+                         _ptr(out.scales))
+        _check(_lib.csa_quant_fp8(ctypes.byref(a), _stream(st)), "csa_quant_fp8")
+    return out
+
+
+def gemm_fp8(x: Fp8Blocks, W: Fp8Blocks, W2: Fp8Blocks = None, *, out=None, out2=None, stream=None):
+    """x [M, K] (block_rows 1) times W [N, K] (block_rows 128), and W2 of the same shape in the same launch.
+    Returns a tuple of one bf16 [M, N] product per weight (out, out2 if given)."""
+    ws = [W] if W2 is None else [W, W2]
+    if not all(isinstance(t, Fp8Blocks) for t in [x, *ws]):
+        raise CSAError("gemm_fp8: the operands are Fp8Blocks")
+    M, K = x.shape
+    N = W.shape[0]
+    if x.block_rows != 1 or any(w.block_rows != 128 for w in ws):
+        raise CSAError("gemm_fp8: x needs block_rows 1, the weights block_rows 128")
+    if any(w.shape != (N, K) for w in ws) or N < 1 or K < 1:
+        raise CSAError(f"gemm_fp8: x {x.shape} and weights {[w.shape for w in ws]} do not fit")
+    if any(w.codes.device != x.codes.device for w in ws):
+        raise CSAError("gemm_fp8: the operands are on different devices")
+    if W2 is None and out2 is not None:
+        raise CSAError("gemm_fp8: out2 without W2")
+    with _On(x.codes, stream) as st:
+        outs = [out, out2][:len(ws)]
+        for i, o in enumerate(outs):
+            if o is None:
+                outs[i] = torch.empty((M, N), dtype=torch.bfloat16, device=x.codes.device)
+            else:
+                _need(o, "gemm_fp8 out", torch.bfloat16, (M, N), x.codes)
+        a = GemmFp8Args(ctypes.sizeof(GemmFp8Args), M, N, K, _ptr(x.codes), _ptr(x.scales))
+        for i, (w, o) in enumerate(zip(ws, outs)):
+            a.W[i], a.W_scales[i], a.out[i] = _ptr(w.codes), _ptr(w.scales), _ptr(o)
+        _check(_lib.csa_gemm_fp8(ctypes.byref(a), _stream(st)), "csa_gemm_fp8")
+    return tuple(outs)
+
+
+def _project_fp8(x, W_kv, W_g, C, Z, stream):
+    """The projection mode of compress() with FP8 weights: C, Z [B, T, d]."""
+    if not (isinstance(W_kv, Fp8Blocks) and isinstance(W_g, Fp8Blocks)) or x is None:
+        raise CSAError("compress: FP8 projections need x and both weights as Fp8Blocks")
+    d = W_kv.shape[0]
+    if isinstance(x, Fp8Blocks):
+        B, T, xq = 1, x.shape[0], x
+    else:
+        _need(x, "compress x", torch.bfloat16, (None, None, W_kv.shape[1]))
+        B, T, xq = x.shape[0], x.shape[1], quant_fp8(x, stream=stream)
+    flat = []
+    for name, t in (("C", C), ("Z", Z)):
+        if t is not None:
+            _need(t, f"compress {name}", torch.bfloat16, (B, T, d), xq.codes)
+            _ptr(t)
+        flat.append(None if t is None else t.view(B * T, d))
+    c, z = gemm_fp8(xq, W_kv, W_g, out=flat[0], out2=flat[1], stream=stream)
+    return c.view(B, T, d), z.view(B, T, d)
+
+
+# -------------------------------------------------------------------------------- caches read back
+
+def _unpack(fn, what, cache, n, n_max, g, row0, idx, out, stream, pages):
+    B, d, d_r = cache.B, cache.d, cache.d_rope
+    if idx is not None:
+        if row0 is not None:
+            raise CSAError(f"{what}: row0 or idx, not both")
+        _need(idx, f"{what} idx", torch.int32, (B, None), cache.codes)
+        if n is not None and n != idx.shape[1]:
+            raise CSAError(f"{what}: n = {n}, but idx holds {idx.shape[1]} ids a sequence")
+        n = idx.shape[1]
+    elif n is None:
+        n = n_max
+    if row0 is not None:
+        _need(row0, f"{what} row0", torch.int32, (B,), cache.codes)
+    with _On(cache.codes, stream) as st:
+        if out is None:
+            out = torch.empty((B, n, d), dtype=torch.bfloat16, device=cache.codes.device)
+        else:
+            _need(out, f"{what} out", torch.bfloat16, (B, n, d), cache.codes)
+        a = UnpackArgs(ctypes.sizeof(UnpackArgs), B, n, d, d_r, n_max, g, _ptr(cache.codes), _ptr(cache.scales),
+                       _ptr(cache.rope) if d_r else None, _ptr(row0), _ptr(idx), _ptr(out), pages)
+        _check(fn(ctypes.byref(a), _stream(st)), what)
+    return out
+
+
+def unpack_fp4(cache, n=None, row0=None, idx=None, out=None, stream=None):
+    """Entries of a PackedCache or PagedCache as bf16 rows [B, n, d]: rows row0[b] + j (row0 int32 [B] or None = 0;
+    n None = all n_max), or the ids idx [B, n] int32.  Ids outside the cache (such as -1) give zero rows."""
+    return _unpack(_lib.csa_unpack_fp4, "csa_unpack_fp4", cache, n, cache.n_max, cache.g, row0, idx, out, stream,
+                   _page_map(cache))
+
+
+def unpack_fp8_window(win: Fp8Window, n=None, row0=None, idx=None, out=None, stream=None):
+    """Rows of an Fp8Window as bf16 [B, n, d]: rows row0[b] + j, or the row numbers idx [B, n] int32 (outside: zero)."""
+    return _unpack(_lib.csa_unpack_fp8_window, "csa_unpack_fp8_window", win, n, win.Wn, 1.0, row0, idx, out, stream,
+                   PageMap())

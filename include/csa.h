@@ -370,6 +370,80 @@ int csa_attn_kernel_count(const csa_attn_args* args, int hca);
 csa_status csa_sparse_attn(const csa_attn_args* args, void* ws, size_t ws_bytes, void* stream);
 csa_status hca_dense_attn(const csa_attn_args* args, void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------------------------------
+ * csa_quant_fp8 — FP8 quantisation in blocks of 128 channels: the operands of csa_gemm_fp8.  The pages fix
+ * FP8 (E4M3) for the stored KV and no scaling; for activations and weights this library uses one fp32 scale per
+ * 128 channels of a row (block_rows = 1) or per block of 128 rows x 128 channels (block_rows = 128):
+ *   scale = fp32(amax / 448) (correctly rounded); code_e = E4M3_rne_satfinite(fp32(x_e / scale)), -0 -> +0;
+ *   an all-zero block has scale 0 and codes 0.  A NaN has no part in amax and becomes the NaN code; an infinity
+ *   makes its block's scale infinite (the block's products are then NaN).
+ * The last block of a row (column) that K (rows) cuts off covers what is there.
+ * Shapes: src[rows][K] bf16; codes[rows][K] u8; scales[ceil(rows / block_rows)][ceil(K / 128)] fp32.
+ * Limits: K % 16 == 0; src and codes 16-byte aligned (else CSA_ERR_UNSUPPORTED).  No workspace.
+ * ------------------------------------------------------------------------------------------------ */
+typedef struct csa_quant_fp8_args {
+  uint32_t struct_size;
+  int32_t rows, K, block_rows;
+  const void* src;
+  uint8_t* codes;
+  float* scales;
+} csa_quant_fp8_args;
+
+csa_status csa_quant_fp8(const csa_quant_fp8_args* args, void* stream);
+
+/* ------------------------------------------------------------------------------------------------
+ * csa_gemm_fp8 — block-scaled FP8 product for one weight or, in one launch, the compressor's two ([V4.1 notes]
+ * CED bullet eq.(1): C and Z are separate projections of the hidden state), E4M3 operands as csa_quant_fp8 writes
+ * them (x with block_rows = 1, each W with block_rows = 128):
+ *   out[w][m][n] = bf16( sum_kb x_scales[m][kb] W_scales[w][n / 128][kb] sum_{k in block kb} x[m][k] W[w][n][k] )
+ * The products of a 128-wide block of K are summed by the tensor cores in fp32, the scaled blocks in fp32 in the
+ * order of kb (split over up to 8 parts of K, added in order, when a launch has few tiles: the result of a shape is
+ * the same at every run).  Weights are [N][K] (K contiguous), the transpose of csa_compress's bf16 W_kv / W_g.
+ * Shapes: x[M][K], W[w][N][K] u8; x_scales[M][KB], W_scales[w][ceil(N / 128)][KB] fp32, KB = ceil(K / 128);
+ *         out[w][M][N] bf16.  W[1], W_scales[1] and out[1] are all NULL for one weight.
+ * Limits: K % 16 == 0, N % 8 == 0; x, W and out 16-byte aligned (else CSA_ERR_UNSUPPORTED).  No workspace.
+ * ------------------------------------------------------------------------------------------------ */
+typedef struct csa_gemm_fp8_args {
+  uint32_t struct_size;
+  int32_t M, N, K;
+  const uint8_t* x;
+  const float* x_scales;
+  const uint8_t* W[2];
+  const float* W_scales[2];
+  void* out[2];
+} csa_gemm_fp8_args;
+
+csa_status csa_gemm_fp8(const csa_gemm_fp8_args* args, void* stream);
+
+/* ------------------------------------------------------------------------------------------------
+ * csa_unpack_fp4 / csa_unpack_fp8_window — cache rows back as bf16 ([V4.1 notes] FP4 主 KV キャッシュ bullet: the
+ * formats that csa_pack_fp4 and csa_pack_fp8_window write).  Output row j of sequence b is cache row idx[b][j], or
+ * row0[b] + j when idx is NULL:
+ *   FP4:  out = bf16(fp32(e2m1 * e4m3 * global_scale)) for the first d - d_rope channels (exact when the global
+ *         scale is a power of two, as the attention reads the entry then);
+ *   FP8:  out = bf16(fp32(e4m3 * scale)) (as the attention reads a window row);
+ *   the last d_rope channels are copied.  A row outside [0, n_max), or on a page outside the pool, reads as zero.
+ * Shapes: as csa_pack_fp4 (scales u8) / csa_pack_fp8_window (scales fp32, n_max = its Wn, no pages, global_scale
+ *         unused); idx[B][n] int32 or NULL; row0[B] int32 or NULL (= 0), not both; out[B][n][d] bf16.
+ * Limits: (d - d_rope) % 32 == 0 (FP8: % 64), d_rope % 8 == 0; out, codes and rope (FP8: scales too) 16-byte
+ *         aligned, FP4 scales 4-byte aligned.  No workspace.
+ * ------------------------------------------------------------------------------------------------ */
+typedef struct csa_unpack_args {
+  uint32_t struct_size;
+  int32_t B, n, d, d_rope, n_max;
+  float global_scale;
+  const uint8_t* codes;
+  const void* scales;
+  const void* rope;
+  const int32_t* row0;
+  const int32_t* idx;
+  void* out;
+  csa_page_map pages;
+} csa_unpack_args;
+
+csa_status csa_unpack_fp4(const csa_unpack_args* args, void* stream);
+csa_status csa_unpack_fp8_window(const csa_unpack_args* args, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -463,3 +463,52 @@ def lse_merge(out1, lse1, out2, lse2):
     a = np.exp(lse1 - lse)[..., None]
     b = np.exp(lse2 - lse)[..., None]
     return a * out1 + b * out2, lse
+
+
+# --------------------------------------------------------------------------------------------
+# FP8 projections in blocks of 128 channels — [V4.1 notes] CED bullet eq.(1): C and Z are projections of the
+# hidden state; the block format is this library's (the pages fix none)
+# --------------------------------------------------------------------------------------------
+
+FP8_BLOCK = 128
+
+
+def quant_fp8(src, block_rows: int = 1):
+    """src [rows, K] (bf16 values) in blocks of block_rows x 128 channels: scale = fp32(amax / 448), code =
+    E4M3(fp32(x / scale)), an all-zero block has scale 0 and codes 0, -0 written as +0.  A NaN has no part in
+    amax and becomes code 0x7F; an infinite amax makes the scale infinite, the infinities 0x7F and the rest 0.
+    Returns (codes u8 [rows, K], scales float64 (fp32 values) [ceil(rows / block_rows), ceil(K / 128)])."""
+    src = np.asarray(src, np.float64)
+    rows, K = src.shape
+    R, C = -(-rows // block_rows), -(-K // FP8_BLOCK)
+    codes = np.zeros((rows, K), np.uint8)
+    scales = np.zeros((R, C), np.float64)
+    for i in range(R):
+        for j in range(C):
+            sl = (slice(i * block_rows, (i + 1) * block_rows), slice(j * FP8_BLOCK, (j + 1) * FP8_BLOCK))
+            x = src[sl]
+            nan = np.isnan(x)
+            amax = np.max(np.where(nan, 0.0, np.abs(x)))
+            s = fp32(amax) / fp32(448.0)
+            scales[i, j] = s
+            with np.errstate(all="ignore"):
+                q = (fp32(x) / (s if s > 0 else fp32(1.0))).astype(np.float64)
+            nan = np.isnan(q)
+            v = e4m3_rne_satfinite(np.where(nan, 0.0, q))
+            c = e4m3_encode(np.abs(v)) | np.where(v < 0, 0x80, 0).astype(np.uint8)
+            codes[sl] = np.where(nan, 0x7F, c)
+    return codes, scales
+
+
+def dequant_fp8(codes, scales, block_rows: int = 1):
+    """The float64 values of quant_fp8's blocks."""
+    rows, K = codes.shape
+    s = np.repeat(np.repeat(scales, block_rows, 0)[:rows], FP8_BLOCK, 1)[:, :K]
+    return e4m3_decode(codes) * s
+
+
+def gemm_fp8(x_codes, x_scales, w_codes, w_scales):
+    """out[m, n] = sum_k x[m, k] W[n, k] of the dequantised operands, unrounded, and the sum of the terms'
+    magnitudes (the scale of a sum's rounding errors)."""
+    x, w = dequant_fp8(x_codes, x_scales, 1), dequant_fp8(w_codes, w_scales, FP8_BLOCK)
+    return x @ w.T, np.abs(x) @ np.abs(w).T
