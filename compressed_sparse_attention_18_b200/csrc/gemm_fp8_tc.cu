@@ -9,14 +9,20 @@
 // scale and add in fp32 registers while the MMAs of the next block fill the other buffer.
 //
 // Tile: 128 rows of one operand (MMA M) x BN of the other (MMA N) x 128 of K per pipeline stage, both by TMA with
-// the 128-byte swizzle (a row of a stage is exactly one 128-byte line).  Two arrangements:
-//   SWAP = false  the 128 rows are tokens, BN channels: a thread holds one token, its scale is one register;
-//   SWAP = true   the 128 rows are channels, BN tokens: few tokens do not pay for 128, and a CTA's channels share
-//                 one weight scale.
+// the 128-byte swizzle (a row of a stage is exactly one 128-byte line).  Three arrangements:
+//   SWAP = false  the 128 rows are tokens, BN = 128 channels: a thread holds one token, its scale is one register;
+//   SWAP = true   the 128 rows are channels, BN = 16 .. 64 tokens: few tokens do not pay for 128, and a CTA's
+//                 channels share one weight scale;
+//   pairs         (below) two CTAs on 256 tokens x 256 channels.
 // A cluster of ks CTAs can share a tile, each taking a part of K; the partial sums meet in distributed shared
 // memory and are added in rank order (the same result at every run).
-// Warp roles (320 threads): warps 0-7 scale and accumulate (4 lane quadrants x 2 column halves), warp 8 TMA, warp 9
-// MMA.  Every wait is bounded; a wait that gives up records device error 1 and the kernel leaves.
+// Bounds, measured on B200 (replayed graphs, SM clock 1.7 GHz under the power cap): 4096 tokens into two weights of
+// 512 x 4096 24.0 us = 1430 TFLOP/s, 8192 x 4096 x 4096 1690 TFLOP/s.  The same pair kernel without reading the
+// accumulators until the end reaches 1630 / 2000, without the loads as well 1970 / 2300: what is left is the
+// hand-over of two accumulators (all of tensor memory) and the operand traffic.  Few tokens are bound by latency:
+// 32 tokens into the two weights take 5.2 us, 4 MB of weights at the copy rate 0.65 us.
+// Warp roles (384 threads): warps 0-7 scale and accumulate (4 lane quadrants x 2 column halves), warp 8 TMA, warps
+// 9 and 10 MMA, warp 11 tensor memory.  Every wait is bounded; a wait that gives up records device error 1 and the kernel leaves.
 #include "csa_common.cuh"
 #include "sm100.cuh"
 
@@ -25,17 +31,17 @@ namespace csa {
 using namespace sm100;
 
 constexpr int GF_ROWS = 128, GF_BK = 128;
-constexpr int GF_EPI = 256, GF_THREADS = GF_EPI + 64;
+constexpr int GF_EPI = 256, GF_THREADS = GF_EPI + 128;
 constexpr int GF_MAX_CLUSTER = 8;
 constexpr int GF_SC_CHUNK = 16;            // K blocks whose token scales are staged at once (SWAP)
 
 template <int BN>
 struct GfCfg {
-  static constexpr int NB = BN <= 64 ? 4 : 2;               // accumulator buffers
-  static constexpr uint32_t TMEM_COLS = NB * BN < 32 ? 32 : NB * BN;
+  static constexpr int NB = 4;                              // accumulator buffers
+  static constexpr uint32_t TMEM_COLS = NB * BN;
   static constexpr int A_BYTES = GF_ROWS * GF_BK;           // 16 KB
   static constexpr int B_BYTES = BN * GF_BK;
-  static constexpr int STAGES = BN == 256 ? 4 : BN == 128 ? 6 : 8;
+  static constexpr int STAGES = BN == 128 ? 6 : 8;
   static constexpr int STAGE_LD = BN + 4;                   // floats per staged row: no bank conflicts
 };
 
@@ -43,10 +49,9 @@ template <int BN>
 struct GfSmem {
   alignas(1024) uint8_t a[GfCfg<BN>::STAGES][GfCfg<BN>::A_BYTES];
   alignas(1024) uint8_t b[GfCfg<BN>::STAGES][GfCfg<BN>::B_BYTES];
-  alignas(16) float sc[2][GF_SC_CHUNK][BN <= 128 ? BN : 1];  // SWAP: token scales x weight scale
+  alignas(16) float sc[2][GF_SC_CHUNK][BN];  // SWAP: token scales x weight scale
   alignas(8) uint64_t full[GfCfg<BN>::STAGES];
-  uint64_t empty[GfCfg<BN>::STAGES];
-  uint64_t acc_full[GfCfg<BN>::NB];
+  uint64_t mma[GfCfg<BN>::STAGES];           // the stage's MMAs have completed: it is free, its accumulator is full
   uint64_t acc_empty[GfCfg<BN>::NB];
   uint64_t done;
   uint32_t tmem_base;
@@ -120,9 +125,9 @@ __global__ void __launch_bounds__(GF_THREADS, 1)
   const int t0 = (int)blockIdx.x / P.ks, tstep = (int)gridDim.x / P.ks;
   if (threadIdx.x == 0) {
     S.err = 0;
-    for (int s = 0; s < ST; ++s) { mbar_init(&S.full[s], 1); mbar_init(&S.empty[s], 1); }
-    for (int a = 0; a < NB; ++a) { mbar_init(&S.acc_full[a], 1); mbar_init(&S.acc_empty[a], GF_EPI / 32); }
-    mbar_init(&S.done, 1);
+    for (int s = 0; s < ST; ++s) { mbar_init(&S.full[s], 1); mbar_init(&S.mma[s], 1); }
+    for (int a = 0; a < NB; ++a) mbar_init(&S.acc_empty[a], GF_EPI / 32);
+    mbar_init(&S.done, 2);
     fence_mbar_init();
   }
   if (warp == 8 && lane == 0) {
@@ -130,14 +135,13 @@ __global__ void __launch_bounds__(GF_THREADS, 1)
     prefetch_tensormap(&w0map);
     prefetch_tensormap(&w1map);
   }
-  if (warp == 9) { tmem_alloc(&S.tmem_base, Cfg::TMEM_COLS); tmem_relinquish(); }
+  if (warp == 11) { tmem_alloc(&S.tmem_base, Cfg::TMEM_COLS); tmem_relinquish(); }
   pdl_trigger();
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = S.tmem_base;
   bool ok = true;
   pdl_wait();                                // operands may be written by the previous kernel
-
   if (warp == 8) {
     // ------------------------------------------------------------------------ TMA producer
     if (lane == 0) {
@@ -147,7 +151,7 @@ __global__ void __launch_bounds__(GF_THREADS, 1)
         const CUtensorMap* wm = w ? &w1map : &w0map;
         for (int kb = kb0; kb < kb1; ++kb, ++it) {
           const int s = it % ST, f = it / ST;
-          if (f > 0 && !mbar_wait(&S.empty[s], (f - 1) & 1)) { ok = false; break; }
+          if (f > 0 && !mbar_wait(&S.mma[s], (f - 1) & 1)) { ok = false; break; }
           mbar_arrive_expect_tx(&S.full[s], Cfg::A_BYTES + Cfg::B_BYTES);
           tma_load_2d(S.a[s], SWAP ? wm : &xmap, kb * GF_BK, ta * GF_ROWS, &S.full[s]);
           tma_load_2d(S.b[s], SWAP ? &xmap : wm, kb * GF_BK, tb * BN, &S.full[s]);
@@ -159,31 +163,32 @@ __global__ void __launch_bounds__(GF_THREADS, 1)
       for (int i = max(0, issued - ST); i < issued; ++i) mbar_wait(&S.full[i % ST], (i / ST) & 1, 1u << 16);
     }
     __syncwarp();
-  } else if (warp == 9) {
-    // ------------------------------------------------------------------------ MMA issuer
+  } else if (warp == 9 || warp == 10) {
+    // ------------------------------------------------------------------------ MMA issuers
+    // Two threads take the K blocks in turn: a thread's waits and its commit cost about 400 cycles a block, and
+    // few MMAs queue behind the running one, so a single issuer left the tensor pipe idle for half of the time.
     if (lane == 0) {
       const uint32_t idesc = idesc_e4m3(GF_ROWS, BN);
-      int it = 0;
-      for (int t = t0; t < P.tiles && ok; t += tstep) {
-        for (int kb = kb0; kb < kb1; ++kb, ++it) {
-          const int s = it % ST, a = it % NB;
-          if (it >= NB && !mbar_wait(&S.acc_empty[a], (it / NB - 1) & 1)) { ok = false; break; }
-          if (!mbar_wait(&S.full[s], (it / ST) & 1)) { ok = false; break; }
-          tc_fence_after();
-          const uint64_t ad = smem_desc(smem_addr(S.a[s]), 16, 1024, LAYOUT_SW128);
-          const uint64_t bd = smem_desc(smem_addr(S.b[s]), 16, 1024, LAYOUT_SW128);
+      const uint64_t ad0 = smem_desc(smem_addr(S.a[0]), 16, 1024, LAYOUT_SW128);
+      const uint64_t bd0 = smem_desc(smem_addr(S.b[0]), 16, 1024, LAYOUT_SW128);
+      const int nk = kb1 - kb0, ntile = t0 < P.tiles ? (P.tiles - 1 - t0) / tstep + 1 : 0;
+      const long long n = (long long)ntile * nk;
+      for (long long it = warp - 9; it < n; it += 2) {
+        const int s = (int)(it % ST), a = (int)(it % NB);
+        if (it >= NB && !mbar_wait(&S.acc_empty[a], (uint32_t)(it / NB - 1) & 1)) { ok = false; break; }
+        if (!mbar_wait(&S.full[s], (uint32_t)(it / ST) & 1)) { ok = false; break; }
+        tc_fence_after();
+        const uint64_t ad = ad0 + (uint64_t)(s * (Cfg::A_BYTES >> 4)), bd = bd0 + (uint64_t)(s * (Cfg::B_BYTES >> 4));
 #pragma unroll
-          for (int kk = 0; kk < GF_BK / 32; ++kk)
-            mma_f8_ss(tbase + (uint32_t)(a * BN), ad + kk * 2, bd + kk * 2, idesc, kk != 0);
-          mma_commit(&S.empty[s]);
-          mma_commit(&S.acc_full[a]);
-        }
+        for (int kk = 0; kk < GF_BK / 32; ++kk)
+          mma_f8_ss(tbase + (uint32_t)(a * BN), ad + kk * 2, bd + kk * 2, idesc, kk != 0);
+        mma_commit(&S.mma[s]);
       }
       mma_commit(&S.done);
       if (!ok) atomicOr(&S.err, 1u);
     }
     __syncwarp();
-  } else {
+  } else if (warp < 8) {
     // ------------------------------------------------------------------------ scale and accumulate
     const int quad = warp & 3, half = warp >> 2;
     const uint32_t lane_off = (uint32_t)(32 * quad) << 16;
@@ -204,10 +209,18 @@ __global__ void __launch_bounds__(GF_THREADS, 1)
       float acc[CW];
 #pragma unroll
       for (int j = 0; j < CW; ++j) acc[j] = 0.f;
-      float f_next = !SWAP && kb0 < kb1 ? sxr[kb0] * swr[kb0] : 0.f;
+      // scales, read four K blocks ahead of their use
+      float sx4[4], sw4[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        sx4[i] = !SWAP && kb0 + i < kb1 ? __ldg(sxr + kb0 + i) : 0.f;
+        sw4[i] = !SWAP && kb0 + i < kb1 ? __ldg(swr + kb0 + i) : 0.f;
+      }
+#pragma unroll 1
       for (int kb = kb0; kb < kb1; ++kb, ++it) {
-        const float f = f_next;
-        const int rel = kb - kb0;
+        const int rel = kb - kb0, a = it % NB;
+        float f = 0.f;
+        const float* fcol = nullptr;
         if constexpr (SWAP) {
           if (rel % GF_SC_CHUNK == 0) {
             // the factors of the next K blocks, [K block][token]: two buffers, so the one being read by a
@@ -221,17 +234,19 @@ __global__ void __launch_bounds__(GF_THREADS, 1)
             }
             asm volatile("bar.sync 1, 256;" ::: "memory");
           }
-        } else if (kb + 1 < kb1) {
-          f_next = sxr[kb + 1] * swr[kb + 1];    // one block ahead
+          fcol = &S.sc[(rel / GF_SC_CHUNK) & 1][rel % GF_SC_CHUNK][half * CW];
+        } else {
+          f = sx4[0] * sw4[0];
+#pragma unroll
+          for (int i = 0; i < 3; ++i) { sx4[i] = sx4[i + 1]; sw4[i] = sw4[i + 1]; }
+          if (kb + 4 < kb1) { sx4[3] = __ldg(sxr + kb + 4); sw4[3] = __ldg(swr + kb + 4); }
         }
-        const int a = it % NB;
-        ok = ok && mbar_wait(&S.acc_full[a], (it / NB) & 1);
+        ok = ok && mbar_wait(&S.mma[it % ST], (it / ST) & 1);
         tc_fence_after();
-        const float* fcol = SWAP ? &S.sc[(rel / GF_SC_CHUNK) & 1][rel % GF_SC_CHUNK][half * CW] : nullptr;
         gf_accumulate<CW, SWAP>(tbase + lane_off + (uint32_t)(a * BN + half * CW), f, fcol, acc);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&S.acc_empty[a]);
+        if (lane == 0) mbar_arrive_relaxed(&S.acc_empty[a]);
       }
       uint16_t* out = w ? P.out[1] : P.out[0];
       if (!SWAP && P.ks == 1) {
@@ -297,13 +312,185 @@ __global__ void __launch_bounds__(GF_THREADS, 1)
     if (P.ks > 1) cluster_sync_all();            // the peers have read this CTA's shared memory
   }
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 11) {
     // every MMA this CTA issued has completed before its tensor memory is released
     mbar_wait(&S.done, 0, 1u << 20);
     tc_fence_after();
     tmem_dealloc(tbase, Cfg::TMEM_COLS);
   }
   if (S.err && threadIdx.x == 0) atomicOr(&g_csa_device_error, 1u);
+}
+
+// ---------------------------------------------------------------------------------------------- CTA pairs
+// The same product with two CTAs to a tile of 256 tokens x BN channels (cta_group::2): each CTA loads its own 128
+// tokens and half of the channels and keeps the accumulators of its own tokens, so a K block brings 128 + BN/2 rows
+// into an SM instead of 128 + BN, and the MMA reads as many.  The even CTA issues the MMAs for both.
+struct GpCfg {
+  static constexpr int BN = 256;
+  static constexpr int NB = 512 / BN;                       // accumulator buffers: all of tensor memory
+  static constexpr int A_BYTES = GF_ROWS * GF_BK;
+  static constexpr int B_BYTES = BN / 2 * GF_BK;
+  static constexpr int STAGES = 6;
+};
+
+struct GpSmem {
+  alignas(1024) uint8_t a[GpCfg::STAGES][GpCfg::A_BYTES];
+  alignas(1024) uint8_t b[GpCfg::STAGES][GpCfg::B_BYTES];
+  alignas(8) uint64_t full[GpCfg::STAGES];   // even CTA: both CTAs' operands of the stage have landed
+  uint64_t mma[GpCfg::STAGES];               // both: the stage's MMAs have completed
+  uint64_t acc_empty[GpCfg::NB];             // even CTA: both CTAs' warps have read the accumulator
+  uint64_t done;                                 // both: all MMAs have completed
+  uint32_t tmem_base;
+  uint32_t err;
+};
+
+__device__ __forceinline__ void mma_f8_ss_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile("{ .reg .pred p; setp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p; }"
+               ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc) : "memory");
+}
+
+__global__ void __launch_bounds__(GF_THREADS, 1) __cluster_dims__(2, 1, 1)
+    gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap w0map,
+                         const __grid_constant__ CUtensorMap w1map, const GfParams P) {
+  using Cfg = GpCfg;
+  constexpr int BN = Cfg::BN, ST = Cfg::STAGES, NB = Cfg::NB, CW = BN / 2;
+  extern __shared__ uint8_t smem_raw[];
+  GpSmem& S = *reinterpret_cast<GpSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)blockIdx.x & 1;
+  const int t0 = (int)blockIdx.x >> 1, tstep = (int)gridDim.x >> 1;
+  const int KB = P.KB;
+  if (threadIdx.x == 0) {
+    S.err = 0;
+    for (int s = 0; s < ST; ++s) { mbar_init(&S.full[s], 1); mbar_init(&S.mma[s], 1); }
+    for (int a = 0; a < NB; ++a) mbar_init(&S.acc_empty[a], 2 * (GF_EPI / 32));
+    mbar_init(&S.done, 2);
+    fence_mbar_init();
+  }
+  if (warp == 8 && lane == 0) {
+    prefetch_tensormap(&xmap);
+    prefetch_tensormap(&w0map);
+    prefetch_tensormap(&w1map);
+  }
+  if (warp == 11) { tmem_alloc_pair(&S.tmem_base, 512); tmem_relinquish_pair(); }
+  pdl_trigger();
+  __syncthreads();
+  cluster_sync_all();                        // both CTAs' barriers and tensor memory are there
+  tc_fence_after();
+  const uint32_t tbase = S.tmem_base;
+  bool ok = true;
+  pdl_wait();
+
+  if (warp == 8) {
+    // ------------------------------------------------------------------------ TMA producer (one per CTA)
+    // 128 sums a thread need more than an even share of the registers: 8 x 232 + 4 x 40 = 12 x 168 warps' worth
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (lane == 0) {
+      int it = 0;
+      for (int t = t0; t < P.tiles && ok; t += tstep) {
+        const int tb = t % P.tiles_b, ta = t / P.tiles_b % P.tiles_a, w = t / P.tiles_b / P.tiles_a;
+        const CUtensorMap* wm = w ? &w1map : &w0map;
+        for (int kb = 0; kb < KB; ++kb, ++it) {
+          const int s = it % ST, f = it / ST;
+          if (f > 0 && !mbar_wait(&S.mma[s], (f - 1) & 1)) { ok = false; break; }
+          if (rank == 0) mbar_arrive_expect_tx(&S.full[s], 2 * (Cfg::A_BYTES + Cfg::B_BYTES));
+          const uint32_t bar = peer_addr(&S.full[s], 0);
+          tma_load_2d_pair(S.a[s], &xmap, kb * GF_BK, (2 * ta + rank) * GF_ROWS, bar);
+          tma_load_2d_pair(S.b[s], wm, kb * GF_BK, tb * BN + rank * (BN / 2), bar);
+        }
+      }
+      if (!ok) atomicOr(&S.err, 1u);
+      // drain: the pair's copies complete before it may leave
+      if (rank == 0)
+        for (int i = max(0, it - ST); i < it; ++i) mbar_wait(&S.full[i % ST], (i / ST) & 1, 1u << 16);
+    }
+    __syncwarp();
+  } else if (warp == 9 || warp == 10) {
+    // ------------------------------------------------------------------------ MMA issuers (even CTA)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (lane == 0 && rank == 0) {
+      const uint32_t idesc = idesc_e4m3(2 * GF_ROWS, BN);
+      const uint64_t ad0 = smem_desc(smem_addr(S.a[0]), 16, 1024, LAYOUT_SW128);
+      const uint64_t bd0 = smem_desc(smem_addr(S.b[0]), 16, 1024, LAYOUT_SW128);
+      const int ntile = t0 < P.tiles ? (P.tiles - 1 - t0) / tstep + 1 : 0;
+      const long long n = (long long)ntile * KB;
+      for (long long it = warp - 9; it < n; it += 2) {
+        const int s = (int)(it % ST), a = (int)(it % NB);
+        if (it >= NB && !mbar_wait(&S.acc_empty[a], (uint32_t)(it / NB - 1) & 1)) { ok = false; break; }
+        if (!mbar_wait(&S.full[s], (uint32_t)(it / ST) & 1)) { ok = false; break; }
+        tc_fence_after();
+        const uint64_t ad = ad0 + (uint64_t)(s * (Cfg::A_BYTES >> 4)), bd = bd0 + (uint64_t)(s * (Cfg::B_BYTES >> 4));
+#pragma unroll
+        for (int kk = 0; kk < GF_BK / 32; ++kk)
+          mma_f8_ss_pair(tbase + (uint32_t)(a * BN), ad + kk * 2, bd + kk * 2, idesc, kk != 0);
+        mma_commit_pair(&S.mma[s]);
+      }
+      mma_commit_pair(&S.done);
+      if (!ok) atomicOr(&S.err, 1u);
+    }
+    __syncwarp();
+  } else if (warp < 8) {
+    // ------------------------------------------------------------------------ scale and accumulate
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+    const int quad = warp & 3, half = warp >> 2;
+    const uint32_t taddr = tbase + ((uint32_t)(32 * quad) << 16) + (uint32_t)(half * CW);
+    const int arow = 32 * quad + lane;
+    const uint32_t empty0 = peer_addr(&S.acc_empty[0], 0);
+    int it = 0;
+    for (int t = t0; t < P.tiles; t += tstep) {
+      const int tb = t % P.tiles_b, ta = t / P.tiles_b % P.tiles_a, w = t / P.tiles_b / P.tiles_a;
+      const int m = (2 * ta + rank) * GF_ROWS + arow, n0 = tb * BN + half * CW;
+      const float* sxr = P.sx + (long long)min(m, P.M - 1) * KB;
+      const float* swr = (w ? P.sw[1] : P.sw[0]) + (long long)min(n0 / 128, (P.N - 1) / 128) * KB;
+      float acc[CW];
+#pragma unroll
+      for (int j = 0; j < CW; ++j) acc[j] = 0.f;
+      // scales, read four K blocks ahead of their use
+      float sx4[4], sw4[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        sx4[i] = i < KB ? __ldg(sxr + i) : 0.f;
+        sw4[i] = i < KB ? __ldg(swr + i) : 0.f;
+      }
+#pragma unroll 1
+      for (int kb = 0; kb < KB; ++kb, ++it) {
+        const int a = it % NB;
+        const float f = sx4[0] * sw4[0];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) { sx4[i] = sx4[i + 1]; sw4[i] = sw4[i + 1]; }
+        if (kb + 4 < KB) { sx4[3] = __ldg(sxr + kb + 4); sw4[3] = __ldg(swr + kb + 4); }
+        ok = ok && mbar_wait(&S.mma[it % ST], (it / ST) & 1);
+        tc_fence_after();
+        gf_accumulate<CW, false>(taddr + (uint32_t)(a * BN), f, nullptr, acc);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_relaxed_cluster(empty0 + 8 * a);
+      }
+      if (m < P.M) {
+        uint16_t* dst = (w ? P.out[1] : P.out[0]) + (long long)m * P.N + n0;
+#pragma unroll
+        for (int j = 0; j < CW; j += 8)
+          if (n0 + j < P.N)
+            *reinterpret_cast<uint4*>(dst + j) =
+                make_uint4(pack_bf16x2(acc[j], acc[j + 1]), pack_bf16x2(acc[j + 2], acc[j + 3]),
+                           pack_bf16x2(acc[j + 4], acc[j + 5]), pack_bf16x2(acc[j + 6], acc[j + 7]));
+      }
+    }
+    if (!ok && lane == 0) atomicOr(&S.err, 1u);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+  }
+  // every MMA of the pair has completed (they read both CTAs' operands and write both tensor memories), and no
+  // arrival is on its way to a CTA that has left
+  __syncthreads();
+  if (warp == 11 && !mbar_wait(&S.done, 0, 1u << 20) && lane == 0) atomicOr(&S.err, 1u);
+  __syncthreads();
+  if (S.err && threadIdx.x == 0) atomicOr(&g_csa_device_error, 1u);
+  cluster_sync_all();
+  if (warp == 11) {
+    tc_fence_after();
+    tmem_dealloc_pair(tbase, 512);
+  }
 }
 
 static bool encode_2d_u8(CUtensorMap* map, const void* base, uint64_t K, uint64_t rows, uint32_t box_rows) {
@@ -359,6 +546,33 @@ static csa_status launch_gemm_fp8(const csa_gemm_fp8_args* a, int ks, cudaStream
   return launch_status();
 }
 
+static csa_status launch_gemm_fp8_pair(const csa_gemm_fp8_args* a, cudaStream_t st) {
+  constexpr int BN = GpCfg::BN;
+  const int nw = a->W[1] ? 2 : 1;
+  CUtensorMap xm, wm[2];
+  if (!encode_2d_u8(&xm, a->x, a->K, a->M, GF_ROWS)) return CSA_ERR_CUDA;
+  for (int w = 0; w < 2; ++w)
+    if (!encode_2d_u8(&wm[w], a->W[w < nw ? w : 0], a->K, a->N, BN / 2)) return CSA_ERR_CUDA;
+  GfParams P{};
+  P.sx = a->x_scales;
+  for (int w = 0; w < nw; ++w) { P.sw[w] = a->W_scales[w]; P.out[w] = (uint16_t*)a->out[w]; }
+  P.M = a->M; P.N = a->N; P.KB = (a->K + GF_BK - 1) / GF_BK; P.ks = 1;
+  const long long ta = ((long long)a->M + 2 * GF_ROWS - 1) / (2 * GF_ROWS), tb = ((long long)a->N + BN - 1) / BN;
+  const long long tiles = ta * tb * nw;
+  if (tiles > 0x7fffffffLL / 2) return CSA_ERR_UNSUPPORTED;
+  P.tiles_a = (int)ta; P.tiles_b = (int)tb; P.tiles = (int)tiles;
+  int sms = 148;
+  {
+    int dev = 0;
+    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  }
+  const int smem = (int)sizeof(GpSmem) + 1024;
+  static std::atomic<unsigned> attr_done{0};
+  set_smem_once((const void*)gemm_fp8_pair_kernel, smem, attr_done);
+  const long long pairs = tiles < sms / 2 ? tiles : sms / 2;
+  return launch_pdl(gemm_fp8_pair_kernel, dim3((unsigned)(2 * pairs)), dim3(GF_THREADS), smem, st, xm, wm[0], wm[1], P);
+}
+
 }  // namespace csa
 
 using namespace csa;
@@ -375,19 +589,24 @@ extern "C" csa_status csa_gemm_fp8(const csa_gemm_fp8_args* a, void* stream) {
   CSA_SUPPORTED(tensor_map_encoder() != nullptr);
   cudaStream_t st = (cudaStream_t)stream;
   const int KB = (a->K + GF_BK - 1) / GF_BK, nw = a->W[1] ? 2 : 1;
-  if (a->M <= 64) {
-    const long long tiles = (a->N + 127) / 128 * (long long)nw;
+  // Parts of K: doubled while the CTAs still fit one wave, each has a K block, and the clusters find room (GPCs hold
+  // one or two of 8 CTAs; 16 such clusters ran in two waves).  Measured, two weights of 512 x 4096: 32 tokens
+  // 10.2 / 7.5 / 5.8 / 5.2 us in 1 / 2 / 4 / 8 parts, 256 tokens 12.5 / 9.9 / 8.0 / 15.2, 1024 tokens 12.9 / 10.9.
+  auto parts = [&](long long tiles, int most) {
     int ks = 1;
-    while (ks < GF_MAX_CLUSTER && 2 * ks <= KB && tiles * ks * 2 <= 148) ks *= 2;
+    while (ks < most && 2 * ks <= KB && tiles * ks * 2 <= 148) ks *= 2;
+    return ks == 8 && tiles > 14 ? 4 : ks;
+  };
+  if (a->M <= 64) {
+    const long long tiles = ((long long)a->N + 127) / 128 * nw;
+    const int ks = parts(tiles, GF_MAX_CLUSTER);
     if (a->M <= 16) return launch_gemm_fp8<16, true>(a, ks, st);
     if (a->M <= 32) return launch_gemm_fp8<32, true>(a, ks, st);
     return launch_gemm_fp8<64, true>(a, ks, st);
   }
-  const long long tiles128 = ((long long)a->M + 127) / 128 * ((a->N + 127) / 128) * nw;
-  if (tiles128 < 148) {
-    int ks = 1;
-    while (ks < GF_MAX_CLUSTER && 2 * ks <= KB && tiles128 * ks * 2 <= 148) ks *= 2;
-    return launch_gemm_fp8<128, false>(a, ks, st);
-  }
-  return launch_gemm_fp8<256, false>(a, 1, st);
+  // Tiles of 128 x 128 while they fill one wave at most, pairs of CTAs on 256 x 256 beyond: 2048 / 4096 tokens into
+  // two weights of 512 x 4096 take 14.2 / 29.4 us with the former and 15.2 (256 x 128) / 24.0 us with the latter.
+  const long long tiles128 = ((long long)a->M + 127) / 128 * (((long long)a->N + 127) / 128) * nw;
+  if (tiles128 < 148) return launch_gemm_fp8<128, false>(a, parts(tiles128, 4), st);
+  return launch_gemm_fp8_pair(a, st);
 }
