@@ -85,7 +85,7 @@ class QuantFp8Args(ctypes.Structure):
 
 class GemmFp8Args(ctypes.Structure):
     _fields_ = [("struct_size", _u32), ("M", _i32), ("N", _i32), ("K", _i32), ("x", _vp), ("x_scales", _vp),
-                ("W", _vp * 2), ("W_scales", _vp * 2), ("out", _vp * 2)]
+                ("W0", _vp), ("W1", _vp), ("W_scales0", _vp), ("W_scales1", _vp), ("out0", _vp), ("out1", _vp)]
 
 
 class UnpackArgs(ctypes.Structure):
@@ -188,23 +188,20 @@ def _need(t, what, dtype, shape=None, like=None):
         raise CSAError(f"{what}: on {t.device}, the other operands are on {like.device}")
 
 
-class _On:
-    """The device and stream of a call: what it allocates belongs to that stream, its kernels launch on the
-    operands' device whichever device is current."""
-
-    def __init__(self, t, stream):
-        _ptr(t)                                          # a CUDA tensor
-        if stream is not None and stream.device != t.device:
-            raise CSAError(f"the stream is on {stream.device}, the operands are on {t.device}")
-        self.stream = stream if stream is not None else torch.cuda.current_stream(t.device)
-        self._ctx = torch.cuda.stream(self.stream)       # also makes its device current
-
-    def __enter__(self):
-        self._ctx.__enter__()
-        return self.stream
-
-    def __exit__(self, *exc):
-        return self._ctx.__exit__(*exc)
+def _launch(t, stream, call, *args):
+    """call(raw stream, *args) with `t`'s device current and what it allocates belonging to that stream: the given one,
+    or the current one of `t`'s device."""
+    dev = t.get_device()
+    if dev < 0:
+        raise CSAError("tensor is not on a CUDA device (no CPU path)")
+    if stream is None:
+        if dev == torch._C._cuda_getDevice():        # the usual call: nothing to switch (a context costs 10 us)
+            return call(torch._C._cuda_getCurrentRawStream(dev), *args)
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device != t.device:
+        raise CSAError(f"the stream is on {stream.device}, the operands are on {t.device}")
+    with torch.cuda.stream(stream):
+        return call(stream.cuda_stream, *args)
 
 
 # ------------------------------------------------------------------------------------------- API
@@ -484,6 +481,8 @@ class Fp8Blocks:
     """A bf16 matrix quantised by quant_fp8: codes [rows, K] u8 (E4M3) and fp32 scales
     [ceil(rows / block_rows), ceil(K / 128)], block_rows 1 (activations) or 128 (weights)."""
 
+    __slots__ = ("codes", "scales", "block_rows")
+
     def __init__(self, codes, scales, block_rows):
         if block_rows not in (1, 128):
             raise CSAError("Fp8Blocks: block_rows is 1 or 128")
@@ -497,56 +496,65 @@ class Fp8Blocks:
         return tuple(self.codes.shape)
 
 
+def _quant_call(st, src, rows, K, block_rows, out):
+    if out is None:
+        out = Fp8Blocks.__new__(Fp8Blocks)
+        out.codes = src.new_empty((rows, K), dtype=torch.uint8)
+        out.scales = src.new_empty((-(-rows // block_rows), -(-K // 128)), dtype=torch.float32)
+        out.block_rows = block_rows
+    a = QuantFp8Args(ctypes.sizeof(QuantFp8Args), rows, K, block_rows, _ptr(src), _ptr(out.codes), _ptr(out.scales))
+    _check(_lib.csa_quant_fp8(ctypes.byref(a), st), "csa_quant_fp8")
+    return out
+
+
 def quant_fp8(src, *, block_rows=1, out=None, stream=None):
     """Quantise src [..., K] bf16 to E4M3 with one fp32 scale per 128 channels of a row (block_rows = 1) or per
     128 x 128 block (block_rows = 128).  Leading dimensions are rows.  Returns Fp8Blocks (out, if given)."""
-    _need(src, "quant_fp8 src", torch.bfloat16)
-    if src.dim() < 1 or src.shape[-1] < 1:
-        raise CSAError("quant_fp8 src: [..., K] with K >= 1 is needed")
+    if not isinstance(src, torch.Tensor) or src.dtype != torch.bfloat16 or src.dim() < 1 or src.shape[-1] < 1:
+        raise CSAError("quant_fp8 src: a bf16 tensor [..., K] with K >= 1 is needed")
+    if block_rows not in (1, 128):
+        raise CSAError("quant_fp8: block_rows is 1 or 128")
     K = src.shape[-1]
     rows = src.numel() // K
-    with _On(src, stream) as st:
-        if out is None:
-            out = Fp8Blocks(torch.empty((rows, K), dtype=torch.uint8, device=src.device),
-                            torch.empty((-(-rows // block_rows) if block_rows > 0 else 0, -(-K // 128)),
-                                        dtype=torch.float32, device=src.device), block_rows)
-        elif out.shape != (rows, K) or out.block_rows != block_rows or out.codes.device != src.device:
-            raise CSAError(f"quant_fp8 out: {out.shape} with block_rows {out.block_rows} on {out.codes.device}, "
-                           f"expected {(rows, K)} with block_rows {block_rows} on {src.device}")
-        a = QuantFp8Args(ctypes.sizeof(QuantFp8Args), rows, K, block_rows, _ptr(src), _ptr(out.codes),
-                         _ptr(out.scales))
-        _check(_lib.csa_quant_fp8(ctypes.byref(a), _stream(st)), "csa_quant_fp8")
-    return out
+    if out is not None and (out.shape != (rows, K) or out.block_rows != block_rows or out.codes.device != src.device):
+        raise CSAError(f"quant_fp8 out: {out.shape} with block_rows {out.block_rows} on {out.codes.device}, "
+                       f"expected {(rows, K)} with block_rows {block_rows} on {src.device}")
+    return _launch(src, stream, _quant_call, src, rows, K, block_rows, out)
+
+
+def _gemm_call(st, x, W, W2, out, out2):
+    M, K = x.codes.shape
+    N = W.codes.shape[0]
+    if out is None:
+        out = x.scales.new_empty((M, N), dtype=torch.bfloat16)
+    if W2 is not None and out2 is None:
+        out2 = x.scales.new_empty((M, N), dtype=torch.bfloat16)
+    a = GemmFp8Args(ctypes.sizeof(GemmFp8Args), M, N, K, _ptr(x.codes), _ptr(x.scales), _ptr(W.codes),
+                    _ptr(W2.codes) if W2 is not None else None, _ptr(W.scales),
+                    _ptr(W2.scales) if W2 is not None else None, _ptr(out), _ptr(out2))
+    _check(_lib.csa_gemm_fp8(ctypes.byref(a), st), "csa_gemm_fp8")
+    return (out,) if W2 is None else (out, out2)
 
 
 def gemm_fp8(x: Fp8Blocks, W: Fp8Blocks, W2: Fp8Blocks = None, *, out=None, out2=None, stream=None):
     """x [M, K] (block_rows 1) times W [N, K] (block_rows 128), and W2 of the same shape in the same launch.
     Returns a tuple of one bf16 [M, N] product per weight (out, out2 if given)."""
-    ws = [W] if W2 is None else [W, W2]
-    if not all(isinstance(t, Fp8Blocks) for t in [x, *ws]):
+    if not isinstance(x, Fp8Blocks) or not isinstance(W, Fp8Blocks) or not (W2 is None or isinstance(W2, Fp8Blocks)):
         raise CSAError("gemm_fp8: the operands are Fp8Blocks")
-    M, K = x.shape
-    N = W.shape[0]
-    if x.block_rows != 1 or any(w.block_rows != 128 for w in ws):
+    xs, ws = x.codes.shape, W.codes.shape
+    if x.block_rows != 1 or W.block_rows != 128 or (W2 is not None and W2.block_rows != 128):
         raise CSAError("gemm_fp8: x needs block_rows 1, the weights block_rows 128")
-    if any(w.shape != (N, K) for w in ws) or N < 1 or K < 1:
-        raise CSAError(f"gemm_fp8: x {x.shape} and weights {[w.shape for w in ws]} do not fit")
-    if any(w.codes.device != x.codes.device for w in ws):
+    if xs[1] != ws[1] or (W2 is not None and W2.codes.shape != ws) or ws[0] < 1 or ws[1] < 1:
+        raise CSAError(f"gemm_fp8: x {x.shape} and weights {[w.shape for w in (W, W2) if w is not None]} do not fit")
+    dev = x.codes.device
+    if W.codes.device != dev or (W2 is not None and W2.codes.device != dev):
         raise CSAError("gemm_fp8: the operands are on different devices")
     if W2 is None and out2 is not None:
         raise CSAError("gemm_fp8: out2 without W2")
-    with _On(x.codes, stream) as st:
-        outs = [out, out2][:len(ws)]
-        for i, o in enumerate(outs):
-            if o is None:
-                outs[i] = torch.empty((M, N), dtype=torch.bfloat16, device=x.codes.device)
-            else:
-                _need(o, "gemm_fp8 out", torch.bfloat16, (M, N), x.codes)
-        a = GemmFp8Args(ctypes.sizeof(GemmFp8Args), M, N, K, _ptr(x.codes), _ptr(x.scales))
-        for i, (w, o) in enumerate(zip(ws, outs)):
-            a.W[i], a.W_scales[i], a.out[i] = _ptr(w.codes), _ptr(w.scales), _ptr(o)
-        _check(_lib.csa_gemm_fp8(ctypes.byref(a), _stream(st)), "csa_gemm_fp8")
-    return tuple(outs)
+    for o in (out, out2):
+        if o is not None:
+            _need(o, "gemm_fp8 out", torch.bfloat16, (xs[0], ws[0]), x.codes)
+    return _launch(x.codes, stream, _gemm_call, x, W, W2, out, out2)
 
 
 def _project_fp8(x, W_kv, W_g, C, Z, stream):
@@ -571,28 +579,33 @@ def _project_fp8(x, W_kv, W_g, C, Z, stream):
 
 # -------------------------------------------------------------------------------- caches read back
 
-def _unpack(fn, what, cache, n, n_max, g, row0, idx, out, stream, pages):
+def _unpack_call(st, fn, what, cache, n, n_max, g, row0, idx, out, pages):
     B, d, d_r = cache.B, cache.d, cache.d_rope
+    if out is None:
+        out = cache.rope.new_empty((B, n, d))
+    a = UnpackArgs(ctypes.sizeof(UnpackArgs), B, n, d, d_r, n_max, g, _ptr(cache.codes), _ptr(cache.scales),
+                   _ptr(cache.rope) if d_r else None, _ptr(row0), _ptr(idx), _ptr(out), pages)
+    _check(fn(ctypes.byref(a), st), what)
+    return out
+
+
+def _unpack(fn, what, cache, n, n_max, g, row0, idx, out, stream, pages):
     if idx is not None:
         if row0 is not None:
             raise CSAError(f"{what}: row0 or idx, not both")
-        _need(idx, f"{what} idx", torch.int32, (B, None), cache.codes)
+        _need(idx, f"{what} idx", torch.int32, (cache.B, None), cache.codes)
         if n is not None and n != idx.shape[1]:
             raise CSAError(f"{what}: n = {n}, but idx holds {idx.shape[1]} ids a sequence")
         n = idx.shape[1]
     elif n is None:
         n = n_max
+    if n < 0:
+        raise CSAError(f"{what}: n = {n}")
     if row0 is not None:
-        _need(row0, f"{what} row0", torch.int32, (B,), cache.codes)
-    with _On(cache.codes, stream) as st:
-        if out is None:
-            out = torch.empty((B, n, d), dtype=torch.bfloat16, device=cache.codes.device)
-        else:
-            _need(out, f"{what} out", torch.bfloat16, (B, n, d), cache.codes)
-        a = UnpackArgs(ctypes.sizeof(UnpackArgs), B, n, d, d_r, n_max, g, _ptr(cache.codes), _ptr(cache.scales),
-                       _ptr(cache.rope) if d_r else None, _ptr(row0), _ptr(idx), _ptr(out), pages)
-        _check(fn(ctypes.byref(a), _stream(st)), what)
-    return out
+        _need(row0, f"{what} row0", torch.int32, (cache.B,), cache.codes)
+    if out is not None:
+        _need(out, f"{what} out", torch.bfloat16, (cache.B, n, cache.d), cache.codes)
+    return _launch(cache.codes, stream, _unpack_call, fn, what, cache, n, n_max, g, row0, idx, out, pages)
 
 
 def unpack_fp4(cache, n=None, row0=None, idx=None, out=None, stream=None):

@@ -54,7 +54,8 @@ def test_quant_refusals(csa):
 def gemm(csa, W=(A16, None), W_scales=(A16, None), out=(A16, None), **kw):
     a = csa.GemmFp8Args(ctypes.sizeof(csa.GemmFp8Args), 4, 64, 256, A16, A16)
     for i in range(2):
-        a.W[i], a.W_scales[i], a.out[i] = W[i], W_scales[i], out[i]
+        for name, v in (("W", W), ("W_scales", W_scales), ("out", out)):
+            setattr(a, f"{name}{i}", v[i])
     for k, v in kw.items():
         setattr(a, k, v)
     return csa._lib.csa_gemm_fp8(ctypes.byref(a), None)
