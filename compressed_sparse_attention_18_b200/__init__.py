@@ -25,7 +25,7 @@ ENTRY_POINTS = ("csa_status_string", "csa_version", "csa_last_cuda_error", "csa_
                 "csa_topk", "csa_attn_workspace_size", "csa_sparse_attn", "hca_dense_attn",
                 "csa_index_topk_noalloc", "csa_device_status", "csa_check_error_path",
                 "csa_pack_fp8_window", "csa_attn_kernel_count", "csa_quant_fp8", "csa_gemm_fp8", "csa_unpack_fp4",
-                "csa_unpack_fp8_window")
+                "csa_unpack_fp8_window", "csa_shared_attn_workspace_size", "hca_shared_attn")
 # (PagedCache: a paged pool + block table, accepted wherever a PackedCache is)
 
 _u32, _i32, _f32, _vp = ctypes.c_uint32, ctypes.c_int32, ctypes.c_float, ctypes.c_void_p
@@ -94,6 +94,10 @@ class UnpackArgs(ctypes.Structure):
                 ("out", _vp), ("pages", PageMap)]
 
 
+class SharedAttnArgs(ctypes.Structure):
+    _fields_ = [("struct_size", _u32), ("n_prefix", _i32), ("prefix_kv", _vp), ("attn", AttnArgs)]
+
+
 _lib.csa_status_string.restype = ctypes.c_char_p
 _lib.csa_status_string.argtypes = [ctypes.c_int]
 _lib.csa_version.restype = ctypes.c_int
@@ -126,6 +130,10 @@ _lib.csa_attn_kernel_count.argtypes = [ctypes.POINTER(AttnArgs), ctypes.c_int]
 for _name in ("csa_sparse_attn", "hca_dense_attn"):
     getattr(_lib, _name).restype = ctypes.c_int
     getattr(_lib, _name).argtypes = [ctypes.POINTER(AttnArgs), _vp, ctypes.c_size_t, _vp]
+_lib.csa_shared_attn_workspace_size.restype = ctypes.c_size_t
+_lib.csa_shared_attn_workspace_size.argtypes = [ctypes.POINTER(SharedAttnArgs)]
+_lib.hca_shared_attn.restype = ctypes.c_int
+_lib.hca_shared_attn.argtypes = [ctypes.POINTER(SharedAttnArgs), _vp, ctypes.c_size_t, _vp]
 
 
 class CSAError(RuntimeError):
@@ -473,6 +481,65 @@ def attn_kernel_count(q, q_pos, cache, n_c, idx, win_kv, win_pos0, *, ratio, win
     a.flags = (CSA_EARLY_START if early_start else 0) | (CSA_CLUSTER_MERGE if cluster else 0)
     a.out_rope_theta = out_rope_theta
     return _lib.csa_attn_kernel_count(ctypes.byref(a), 1 if hca else 0)
+
+
+# ------------------------------------------------------------------------- HCA with a shared prefix
+
+def _shared_args(q, q_pos, cache, n_c, prefix_kv, win_kv, win_pos0, ratio, window, softmax_scale, out, lse,
+                 out_rope_theta):
+    a = SharedAttnArgs(ctypes.sizeof(SharedAttnArgs), prefix_kv.shape[0], _ptr(prefix_kv))
+    a.attn = _attn_args(q, q_pos, cache, n_c, None, win_kv, win_pos0, ratio, window, softmax_scale, out, lse)
+    a.attn.out_rope_theta = out_rope_theta
+    return a
+
+
+def _shared_call(st, q, q_pos, cache, n_c, prefix_kv, win_kv, win_pos0, ratio, window, softmax_scale, out, lse, ws,
+                 out_rope_theta):
+    if out is None:
+        out = q.new_empty(q.shape)
+    if lse is None:
+        lse = q.new_empty(q.shape[:3], dtype=torch.float32)
+    a = _shared_args(q, q_pos, cache, n_c, prefix_kv, win_kv, win_pos0, ratio, window, softmax_scale, out, lse,
+                     out_rope_theta)
+    nbytes = _lib.csa_shared_attn_workspace_size(ctypes.byref(a))
+    if nbytes and ws is None:
+        ws = q.new_empty((nbytes,), dtype=torch.uint8)
+    have = ws.numel() * ws.element_size() if ws is not None else 0
+    _check(_lib.hca_shared_attn(ctypes.byref(a), _ptr(ws), have, st), "hca_shared_attn")
+    return out, lse
+
+
+def hca_shared_attn(q, q_pos, cache, n_c, prefix_kv, win_kv=None, win_pos0=None, *, ratio=128, window=128,
+                    softmax_scale=0.0, out=None, lse=None, ws=None, out_rope_theta=0.0, stream=None):
+    """hca_attn() for a batch whose sequences share their first entries: prefix_kv [n_prefix, d] bf16 (unpack_fp4 reads
+    it back once) stands for entries [0, n_prefix) of every sequence, cache rows from n_prefix on for the others.
+    n_c counts both.  ws: a workspace of shared_attn_workspace_size() bytes (allocated when None).  Returns (out, lse)."""
+    _need(q, "hca_shared_attn q", torch.bfloat16, (None, None, None, None))
+    B, Nq, H, d = q.shape
+    _need(q_pos, "hca_shared_attn q_pos", torch.int64, (B, Nq), q)
+    _need(n_c, "hca_shared_attn n_c", torch.int32, (B,), q)
+    _need(prefix_kv, "hca_shared_attn prefix_kv", torch.bfloat16, (None, d), q)
+    if cache.B != B or cache.d != d or cache.codes.device != q.device:
+        raise CSAError(f"hca_shared_attn: a cache of {cache.B} sequences of width {cache.d} on {cache.codes.device}, "
+                       f"queries of {B} of width {d} on {q.device}")
+    if win_kv is not None:
+        if not isinstance(win_kv, Fp8Window):
+            _need(win_kv, "hca_shared_attn win_kv", torch.bfloat16, (B, None, d), q)
+        elif win_kv.B != B or win_kv.d != d or win_kv.codes.device != q.device:
+            raise CSAError("hca_shared_attn: the window is of another batch, width or device")
+        _need(win_pos0, "hca_shared_attn win_pos0", torch.int64, (B,), q)
+    if out is not None:
+        _need(out, "hca_shared_attn out", torch.bfloat16, tuple(q.shape), q)
+    if lse is not None:
+        _need(lse, "hca_shared_attn lse", torch.float32, (B, Nq, H), q)
+    return _launch(q, stream, _shared_call, q, q_pos, cache, n_c, prefix_kv, win_kv, win_pos0, ratio, window,
+                   softmax_scale, out, lse, ws, out_rope_theta)
+
+
+def shared_attn_workspace_size(q, q_pos, cache, n_c, prefix_kv, win_kv=None, win_pos0=None, *, ratio=128, window=128):
+    """Bytes of workspace a hca_shared_attn call with these arguments needs."""
+    a = _shared_args(q, q_pos, cache, n_c, prefix_kv, win_kv, win_pos0, ratio, window, 0.0, None, None, 0.0)
+    return _lib.csa_shared_attn_workspace_size(ctypes.byref(a))
 
 
 # ---------------------------------------------------------------------------------- FP8 projections

@@ -579,10 +579,14 @@ static csa_status launch_out_rope(uint16_t* out, int H, int D, long long rows, c
 }
 
 // tensor-core decode path (attn_tc.cu)
-void attn_tc_plan(const csa_attn_args* a, int hca, int* splits, int* tpc);
+void attn_tc_plan(const csa_attn_args* a, int hca, int first, int* splits, int* tpc);
 bool attn_tc_cluster(int splits);
-csa_status launch_attn_tc(const csa_attn_args* a, int hca, int splits, int tpc, uint16_t* part_o, float* part_lse,
-                          cudaStream_t st);
+csa_status launch_attn_tc(const csa_attn_args* a, int hca, int first, int splits, int slots, int tpc, uint16_t* part_o,
+                          float* part_lse, cudaStream_t st);
+// attention over a shared prefix (attn_prefix_tc.cu)
+void attn_prefix_plan(long long R, int n_p, int most, int* ctas, int* slots);
+csa_status launch_attn_prefix(const csa_attn_args* a, const void* prefix, int n_p, int ctas, int slot0, int pslots, int slots,
+                              uint16_t* part_o, float* part_lse, cudaStream_t st);
 
 bool attn_tc_eligible(const csa_attn_args* a, int hca, int max_splits);
 
@@ -598,7 +602,7 @@ static AttnPlan plan_attn(const csa_attn_args* a, int hca) {
   if (attn_tc_eligible(a, hca, MERGE_MAX_SPLITS)) {
     p.tc = true;
     p.cps = 1;
-    attn_tc_plan(a, hca, &p.splits, &p.tpc);
+    attn_tc_plan(a, hca, 0, &p.splits, &p.tpc);
     size_t o = 0;
     const bool cluster = attn_tc_cluster(p.splits) && (a->flags & CSA_CLUSTER_MERGE);
     if (p.splits > 1 && !cluster) {                       // (a cluster merges its query's partials on chip)
@@ -682,7 +686,7 @@ static csa_status run_attn(const csa_attn_args* a, void* ws, size_t ws_bytes, vo
     const bool on_chip = p.splits == 1 || (attn_tc_cluster(p.splits) && (a->flags & CSA_CLUSTER_MERGE));
     uint16_t* po = !on_chip ? (uint16_t*)((uint8_t*)ws + p.off_o) : nullptr;
     float* pl = !on_chip ? (float*)((uint8_t*)ws + p.off_lse) : nullptr;
-    csa_status s = launch_attn_tc(a, hca, p.splits, p.tpc, po, pl, st);
+    csa_status s = launch_attn_tc(a, hca, 0, p.splits, p.splits, p.tpc, po, pl, st);
     if (s != CSA_OK) return s;
     const bool merged = on_chip;
     if (merged)
@@ -719,9 +723,71 @@ static csa_status run_attn(const csa_attn_args* a, void* ws, size_t ws_bytes, vo
                              a->out_rope_theta, st);
 }
 
+// ---- HCA with a shared prefix: the sequences' own keys (entries from n_p on, and the window) by the attention above
+// and the prefix by attn_prefix_tc_kernel, each leaving partials in the query's slots [own | prefix]; one merge.
+struct SharedPlan {
+  int own, tpc;           // splits of the own keys (0: there are none), their tiles per CTA
+  int ctas, pslots;       // the prefix kernel's
+  size_t off_lse, total;
+};
+
+static SharedPlan plan_shared(const csa_shared_attn_args* s) {
+  const csa_attn_args* a = &s->attn;
+  SharedPlan p{};
+  if (a->n_max > s->n_prefix || attn_has_window(a)) attn_tc_plan(a, 1, s->n_prefix, &p.own, &p.tpc);
+  attn_prefix_plan((long long)a->B * a->Nq * a->H, s->n_prefix, MERGE_MAX_SPLITS, &p.ctas, &p.pslots);
+  const size_t parts = (size_t)a->B * a->Nq * (p.own + p.pslots) * a->H;
+  p.off_lse = align_up(parts * 512 * 2, 256);
+  p.total = align_up(p.off_lse + parts * 4, 256);
+  return p;
+}
+
+static csa_status validate_shared(const csa_shared_attn_args* s, bool ptrs) {
+  CSA_REQUIRE(s != nullptr && s->struct_size == sizeof(csa_shared_attn_args));
+  const csa_status v = validate_attn(&s->attn, 1, ptrs);
+  if (v != CSA_OK) return v;
+  CSA_REQUIRE(s->n_prefix >= 0 && s->n_prefix <= s->attn.n_max);
+  CSA_SUPPORTED(s->attn.d == 512 && s->attn.flags == 0);
+  const long long R = (long long)s->attn.B * s->attn.Nq * s->attn.H;
+  CSA_SUPPORTED(R <= 0x7fffffffLL - 128);
+  if (R == 0 || !ptrs) return CSA_OK;
+  CSA_REQUIRE(s->n_prefix == 0 || s->prefix_kv);
+  CSA_SUPPORTED(((uintptr_t)s->prefix_kv & 15) == 0 && attn_tc_eligible(&s->attn, 1, 1 << 30));
+  return CSA_OK;
+}
+
+static csa_status run_shared(const csa_shared_attn_args* s, void* ws, size_t ws_bytes, cudaStream_t st) {
+  const csa_status v = validate_shared(s, true);
+  if (v != CSA_OK) return v;
+  const csa_attn_args* a = &s->attn;
+  if (s->n_prefix == 0) return run_attn(a, ws, ws_bytes, st, 1);
+  const long long rows = (long long)a->B * a->Nq;
+  if (rows == 0) return CSA_OK;
+  const SharedPlan p = plan_shared(s);
+  if (ws_bytes < p.total) return CSA_ERR_WORKSPACE;
+  CSA_REQUIRE(ws != nullptr);
+  uint16_t* po = (uint16_t*)ws;
+  float* pl = (float*)((uint8_t*)ws + p.off_lse);
+  const int slots = p.own + p.pslots;
+  csa_status r = CSA_OK;
+  if (p.own > 0) r = launch_attn_tc(a, 1, s->n_prefix, p.own, slots, p.tpc, po, pl, st);
+  if (r == CSA_OK) r = launch_attn_prefix(a, s->prefix_kv, s->n_prefix, p.ctas, p.own, p.pslots, slots, po, pl, st);
+  if (r != CSA_OK) return r;
+  return launch_merge<uint16_t>(po, pl, slots, a->H, a->d, rows, (uint16_t*)a->out, a->lse, a->q_pos, a->out_rope_theta, st);
+}
+
 }  // namespace csa
 
 using namespace csa;
+
+extern "C" size_t csa_shared_attn_workspace_size(const csa_shared_attn_args* a) {
+  if (validate_shared(a, false) != CSA_OK || (long long)a->attn.B * a->attn.Nq == 0) return 0;
+  return a->n_prefix == 0 ? plan_attn(&a->attn, 1).total : plan_shared(a).total;
+}
+
+extern "C" csa_status hca_shared_attn(const csa_shared_attn_args* a, void* ws, size_t ws_bytes, void* stream) {
+  return run_shared(a, ws, ws_bytes, (cudaStream_t)stream);
+}
 
 extern "C" size_t csa_attn_workspace_size(const csa_attn_args* a, int hca) {
   if (validate_attn(a, hca, false) != CSA_OK) return 0;

@@ -73,15 +73,17 @@ struct TaParams {
   const int32_t* idx;
   const uint16_t* win;
   const int64_t* win_pos0;
-  uint16_t* out;        // splits == 1
-  float* lse;           // splits == 1 (may be null)
-  uint16_t* part_o;     // [rows][splits][H][512] bf16 (splits = CTAs per query)
-  float* part_lse;      // [rows][splits][H]
+  uint16_t* out;        // part_o == null
+  float* lse;           // part_o == null (may be null)
+  uint16_t* part_o;     // [rows][slots][H][512] bf16 (slot = split: CTAs per query); null: whole queries, to out / lse
+  float* part_lse;      // [rows][slots][H]
   int win_fp8;          // window rows are FP8 (codes / scales / rope below) instead of bf16 rows in `win`
   const uint8_t* wcodes;   // [B][Wn][448] E4M3
   const float* wscales;    // [B][Wn][8] fp32 (7 used)
   const uint16_t* wrope;   // [B][Wn][64] bf16
   csa_page_map pm;         // cache rows (table == NULL: contiguous [B][n_max])
+  int first;               // hca: the first entry of the key list (earlier ones are attended elsewhere)
+  int slots;               // partials a query has in part_o / part_lse (its splits, or more: others write the rest)
 };
 
 __device__ __forceinline__ uint32_t sw128(int row, int chunk) { return (uint32_t)(row * 128 + ((chunk ^ (row & 7)) << 4)); }
@@ -261,7 +263,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
   int n_sel = P.k;
   if (P.hca) {                                   // all visible entries: r*i + r - 1 <= t and i < n_c
     long long nv = (tq + 1) / P.ratio;
-    n_sel = (int)max(0LL, min(nv, (long long)ncb));
+    n_sel = (int)max(0LL, min(nv, (long long)ncb) - P.first);
   }
   long long wlo = 0, whi = -1;
   if (P.Wn > 0) {
@@ -269,7 +271,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
     whi = min(tq, p0 + P.Wn - 1);
   }
   const int n_list = n_sel + (whi >= wlo ? (int)(whi - wlo + 1) : 0);
-  const size_t unit_ho = ((size_t)bq * P.splits + split) * P.H;
+  const size_t unit_ho = ((size_t)bq * P.slots + split) * P.H;
   // this CTA's tiles (block-uniform): up to tpc consecutive tiles of the key list from split*tpc; with the
   // early window the splits cover the entries only and split 0 takes the window tile first (n_sel is
   // then a multiple of the tile)
@@ -286,7 +288,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
   const uint32_t tb = S.tmem_base;
 
   if (ntile == 0 && !P.cluster) {               // nothing in this CTA's tiles: an empty partial
-    if (P.splits > 1) {
+    if (P.part_o != nullptr) {
       if (tid < P.H) P.part_lse[unit_ho + tid] = -INFINITY;
     } else {
       for (int i = tid; i < P.H * 256; i += TA_THREADS)
@@ -371,7 +373,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
     auto raw_id = [&](const TaTile& g) -> int {
       const int li = g.key0 + grow;
       if (grow >= g.rs) return -1;
-      return P.hca ? li : (li < P.k ? P.idx[(size_t)bq * P.k + li] : -1);
+      return P.hca ? P.first + li : (li < P.k ? P.idx[(size_t)bq * P.k + li] : -1);
     };
     auto check_id = [&](int v) -> int { return (v >= 0 && v < ncb) ? v : -1; };
     uint4 cv[7], sc16, rp[4];
@@ -649,7 +651,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
       if (P.cluster) {
 #pragma unroll
         for (int j = 0; j < 32; ++j) stage[(hh * 32 + j) * 512 + dim] = __uint_as_float(ov[j]);
-      } else if (P.splits == 1) {
+      } else if (P.part_o == nullptr) {
         uint16_t* o = P.out + ((size_t)bq * P.H + hh * 32) * 512 + dim;
 #pragma unroll
         for (int j = 0; j < 32; ++j)
@@ -665,7 +667,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
     if (tid < P.H && !P.cluster) {
       const float lh = S.l[tid];
       const float ls = lh > 0.f ? (S.m[tid] + log2f(lh)) * TA_LN2 : -INFINITY;
-      if (P.splits == 1) {
+      if (P.part_o == nullptr) {
         if (P.lse) P.lse[(size_t)bq * P.H + tid] = ls;
       } else {
         P.part_lse[unit_ho + tid] = ls;
@@ -774,6 +776,11 @@ struct TaUnit {
   int wofs;             // window buffer row of the first window key (wlo - win_pos0)
 };
 
+// Place of a unit's partial: its query's slots, then its split.
+__device__ __forceinline__ size_t ta_part(const TaParams& P, int uid) {
+  return (size_t)(uid / P.splits) * P.slots + uid % P.splits;
+}
+
 __device__ __forceinline__ TaUnitRaw ta_unit_load(const TaParams& P, int uid) {
   TaUnitRaw r;
   const int bq = uid / P.splits, b = bq / P.Nq;
@@ -793,7 +800,7 @@ __device__ __forceinline__ TaUnit ta_unit(const TaParams& P, const TaUnitRaw& r)
   u.b = u.bq / P.Nq;
   u.ncb = min(r.nc, P.n_max);
   u.n_sel = P.k;
-  if (P.hca) u.n_sel = (int)max(0LL, min((r.tq + 1) / P.ratio, (long long)u.ncb));
+  if (P.hca) u.n_sel = (int)max(0LL, min((r.tq + 1) / P.ratio, (long long)u.ncb) - P.first);
   long long wlo = 0, whi = -1;
   if (P.Wn > 0) {
     wlo = max(max(0LL, r.tq - P.window + 1), r.wp0);
@@ -824,8 +831,8 @@ __device__ __forceinline__ TaUnit ta_next_unit(const TaParams& P, int kk, int nu
     if (raw.uid != uid) raw = ta_unit_load(P, uid);
     uu = ta_unit(P, raw);
     if (uu.ntile > 0) return uu;
-    if (P.splits > 1) {
-      if (tid < P.H) P.part_lse[(size_t)uid * P.H + tid] = -INFINITY;
+    if (P.part_o != nullptr) {
+      if (tid < P.H) P.part_lse[ta_part(P, uid) * P.H + tid] = -INFINITY;
     } else {
       for (int i = tid; i < P.H * 256; i += nthreads)
         reinterpret_cast<uint32_t*>(P.out + (size_t)uu.bq * P.H * 512)[i] = 0u;
@@ -843,9 +850,9 @@ __device__ __forceinline__ TaUnit ta_next_unit(const TaParams& P, int kk, int nu
 __device__ __forceinline__ bool ta_epilogue(TaSmem& S, const TaParams& P, int uid, uint32_t par, uint32_t lane_base,
                                             int hh, int quad, int lane, int tid) {
   bool ok = true;
-  const bool part = P.splits > 1;
-  uint16_t* orow = part ? P.part_o + (size_t)uid * P.H * 512 : P.out + (size_t)uid * P.H * 512;
-  float* lrow = part ? P.part_lse + (size_t)uid * P.H : (P.lse ? P.lse + (size_t)uid * P.H : nullptr);
+  const bool part = P.part_o != nullptr;
+  uint16_t* orow = part ? P.part_o + ta_part(P, uid) * P.H * 512 : P.out + (size_t)uid * P.H * 512;
+  float* lrow = part ? P.part_lse + ta_part(P, uid) * P.H : (P.lse ? P.lse + (size_t)uid * P.H : nullptr);
   if (tid < 64) {
     const float lh = S.l[tid];
     S.fac[tid] = lh > 0.f ? 1.f / lh : 0.f;
@@ -1042,7 +1049,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
     auto raw_id = [&](const TaUnit& uu, const TaTile& gg) -> int {
       if (grow >= gg.rs) return -1;
       const int li = gg.key0 + grow;
-      return P.hca ? li : (li < P.k ? P.idx[(size_t)uu.bq * P.k + li] : -1);
+      return P.hca ? P.first + li : (li < P.k ? P.idx[(size_t)uu.bq * P.k + li] : -1);
     };
     auto check_id = [&](const TaUnit& uu, int v) -> int { return (v >= 0 && v < uu.ncb) ? v : -1; };
     // the first query with keys at or after unit kk (from its raw positions, if they are those of unit
@@ -1304,10 +1311,11 @@ static int attn_tc_persist_tpc(long long rows, long long tiles, int H) {
 // one wave of the 148 SMs, else enough tiles per CTA (walked in order, online softmax) to come back to one
 // wave; with the early window the entry tiles alone are planned this way and split 0 also takes the window
 // tile (first, while the previous kernel still runs).  Persistent kernel: see attn_tc_persist_tpc.
-void attn_tc_plan(const csa_attn_args* a, int hca, int* splits, int* tpc) {
+// `first` (hca): entries before it are not attended here.
+void attn_tc_plan(const csa_attn_args* a, int hca, int first, int* splits, int* tpc) {
   const bool early = attn_tc_early(a, hca);
   const long long n_win = attn_has_window(a) ? (a->Wn < a->window ? a->Wn : a->window) : 0;
-  const long long n = (hca ? a->n_max : a->k) + (early ? 0 : n_win);
+  const long long n = (hca ? a->n_max - first : a->k) + (early ? 0 : n_win);
   const long long tiles = n > 0 ? (n + TA_KEYS - 1) / TA_KEYS : 1;
   const long long rows = (long long)a->B * a->Nq;
   long long t;
@@ -1323,11 +1331,10 @@ void attn_tc_plan(const csa_attn_args* a, int hca, int* splits, int* tpc) {
 }
 
 // The persistent kernel's plans (the same decision attn_tc_plan made).
-bool attn_tc_persistent(const csa_attn_args* a, int hca, int splits) {
-  (void)splits;
+bool attn_tc_persistent(const csa_attn_args* a, int hca, int first) {
   const bool early = attn_tc_early(a, hca);
   const long long n_win = attn_has_window(a) ? (a->Wn < a->window ? a->Wn : a->window) : 0;
-  const long long n = (hca ? a->n_max : a->k) + (early ? 0 : n_win);
+  const long long n = (hca ? a->n_max - first : a->k) + (early ? 0 : n_win);
   const long long tiles = n > 0 ? (n + TA_KEYS - 1) / TA_KEYS : 1;
   return attn_tc_persist_ok(a, hca, (long long)a->B * a->Nq, tiles);
 }
@@ -1338,7 +1345,7 @@ bool attn_tc_cluster(int splits) { return splits >= 2 && splits <= TA_MAX_CLUSTE
 
 bool attn_tc_eligible(const csa_attn_args* a, int hca, int max_splits) {
   int splits = 0, tpc = 0;
-  attn_tc_plan(a, hca, &splits, &tpc);
+  attn_tc_plan(a, hca, 0, &splits, &tpc);
   return a->d == 512 && a->d_rope == 64 && a->H <= 64 && splits >= 1 && splits <= max_splits &&
          ((uintptr_t)a->q & 15) == 0 && (a->n_max == 0 || (((uintptr_t)a->kv_codes & 15) == 0 &&
                                                            ((uintptr_t)a->kv_rope & 15) == 0)) &&
@@ -1349,7 +1356,8 @@ bool attn_tc_eligible(const csa_attn_args* a, int hca, int max_splits) {
          tensor_map_encoder() != nullptr;
 }
 
-csa_status launch_attn_tc(const csa_attn_args* a, int hca, int splits, int tpc, uint16_t* part_o,
+// first, slots: see TaParams (0 and splits for an attention of its own).
+csa_status launch_attn_tc(const csa_attn_args* a, int hca, int first, int splits, int slots, int tpc, uint16_t* part_o,
                           float* part_lse, cudaStream_t st) {
   const long long rows = (long long)a->B * a->Nq;
   CUtensorMap qmap, wmap;
@@ -1379,9 +1387,9 @@ csa_status launch_attn_tc(const csa_attn_args* a, int hca, int splits, int tpc, 
   }
   TaParams P{};
   P.Nq = a->Nq; P.H = a->H; P.ratio = a->ratio; P.n_max = a->n_max; P.k = hca ? 0 : a->k; P.rows = (int)rows;
-  P.Wn = Wn; P.window = a->window; P.splits = splits; P.tpc = tpc; P.hca = hca; P.g = a->g_kv;
+  P.Wn = Wn; P.window = a->window; P.splits = splits; P.slots = slots; P.first = first; P.tpc = tpc; P.hca = hca; P.g = a->g_kv;
   P.early_rows = attn_tc_early(a, hca) ? (int)rows : 0;
-  P.cluster = (attn_tc_cluster(splits) && (a->flags & CSA_CLUSTER_MERGE)) ? 1 : 0;
+  P.cluster = (part_o == nullptr && attn_tc_cluster(splits)) ? 1 : 0;   // (asked for by CSA_CLUSTER_MERGE)
   const float scale = a->softmax_scale != 0.0f ? a->softmax_scale : 1.0f / sqrtf((float)a->d);
   P.scale_log2 = scale * TA_LOG2E;
   P.q_pos = a->q_pos; P.codes = a->kv_codes; P.scales = a->kv_scales;
@@ -1396,7 +1404,7 @@ csa_status launch_attn_tc(const csa_attn_args* a, int hca, int splits, int tpc, 
     P.wrope = (const uint16_t*)a->win_rope;
   }
   const int smem = (int)sizeof(TaSmem) + 1024;
-  if (attn_tc_persistent(a, hca, splits)) {
+  if (attn_tc_persistent(a, hca, first)) {
     // one persistent CTA per SM walks its units (query, split) back to back
     int sms = 148;
     {

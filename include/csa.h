@@ -444,6 +444,30 @@ typedef struct csa_unpack_args {
 csa_status csa_unpack_fp4(const csa_unpack_args* args, void* stream);
 csa_status csa_unpack_fp8_window(const csa_unpack_args* args, void* stream);
 
+/* ------------------------------------------------------------------------------------------------
+ * hca_shared_attn — hca_dense_attn for a batch whose sequences begin with the same prefix ([V4 blog] Fig. 4: the
+ * 128x layer attends densely over all visible entries; a shared prompt makes the first n_prefix of them the same for
+ * every sequence).  Entries [0, n_prefix) of every sequence are prefix_kv (bf16 rows [n_prefix][d], such as
+ * csa_unpack_fp4 reads back once when the prefix is written); the cache holds the others.  With
+ * prefix_kv = the cache's own first rows the result is hca_dense_attn's, up to rounding.
+ *   attn: the arguments of hca_dense_attn.  Entry numbers stay the sequence's own: n_c[b] counts the prefix, entry i
+ *         is visible iff i < n_c[b] and ratio*i + ratio - 1 <= t, and rows [0, n_prefix) of the cache are never read
+ *         (a paged cache needs no pages for the whole pages among them).  flags must be 0.
+ * Every row of prefix_kv must hold finite values (rows a query does not see get weight exactly 0).
+ * Limits: d = 512, H <= 64, 0 <= n_prefix <= n_max, B * Nq * H < 2^31 - 128; q, prefix_kv, the cache and the window
+ *         16-byte aligned (else CSA_ERR_UNSUPPORTED).
+ * Workspace: csa_shared_attn_workspace_size() (partials).  Results do not depend on what the workspace held.
+ * ------------------------------------------------------------------------------------------------ */
+typedef struct csa_shared_attn_args {
+  uint32_t struct_size;
+  int32_t n_prefix;
+  const void* prefix_kv;
+  csa_attn_args attn;
+} csa_shared_attn_args;
+
+size_t csa_shared_attn_workspace_size(const csa_shared_attn_args* args);
+csa_status hca_shared_attn(const csa_shared_attn_args* args, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
