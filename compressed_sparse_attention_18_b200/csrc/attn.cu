@@ -584,8 +584,8 @@ bool attn_tc_cluster(int splits);
 csa_status launch_attn_tc(const csa_attn_args* a, int hca, int first, int splits, int slots, int tpc, uint16_t* part_o,
                           float* part_lse, cudaStream_t st);
 // attention over a shared prefix (attn_prefix_tc.cu)
-void attn_prefix_plan(long long R, int n_p, int most, int* ctas, int* slots);
-csa_status launch_attn_prefix(const csa_attn_args* a, const void* prefix, int n_p, int ctas, int slot0, int pslots, int slots,
+void attn_prefix_plan(long long R, int n_p, int most, int* pairs, int* slots);
+csa_status launch_attn_prefix(const csa_attn_args* a, const void* prefix, int n_p, int pairs, int slot0, int pslots, int slots,
                               uint16_t* part_o, float* part_lse, cudaStream_t st);
 
 bool attn_tc_eligible(const csa_attn_args* a, int hca, int max_splits);
@@ -727,7 +727,7 @@ static csa_status run_attn(const csa_attn_args* a, void* ws, size_t ws_bytes, vo
 // and the prefix by attn_prefix_tc_kernel, each leaving partials in the query's slots [own | prefix]; one merge.
 struct SharedPlan {
   int own, tpc;           // splits of the own keys (0: there are none), their tiles per CTA
-  int ctas, pslots;       // the prefix kernel's
+  int pairs, pslots;      // the prefix kernel's
   size_t off_lse, total;
 };
 
@@ -735,7 +735,7 @@ static SharedPlan plan_shared(const csa_shared_attn_args* s) {
   const csa_attn_args* a = &s->attn;
   SharedPlan p{};
   if (a->n_max > s->n_prefix || attn_has_window(a)) attn_tc_plan(a, 1, s->n_prefix, &p.own, &p.tpc);
-  attn_prefix_plan((long long)a->B * a->Nq * a->H, s->n_prefix, MERGE_MAX_SPLITS, &p.ctas, &p.pslots);
+  attn_prefix_plan((long long)a->B * a->Nq * a->H, s->n_prefix, MERGE_MAX_SPLITS, &p.pairs, &p.pslots);
   const size_t parts = (size_t)a->B * a->Nq * (p.own + p.pslots) * a->H;
   p.off_lse = align_up(parts * 512 * 2, 256);
   p.total = align_up(p.off_lse + parts * 4, 256);
@@ -747,6 +747,7 @@ static csa_status validate_shared(const csa_shared_attn_args* s, bool ptrs) {
   const csa_status v = validate_attn(&s->attn, 1, ptrs);
   if (v != CSA_OK) return v;
   CSA_REQUIRE(s->n_prefix >= 0 && s->n_prefix <= s->attn.n_max);
+  CSA_REQUIRE(s->attn.softmax_scale >= 0.0f);    // (false for NaN too)
   CSA_SUPPORTED(s->attn.d == 512 && s->attn.flags == 0);
   const long long R = (long long)s->attn.B * s->attn.Nq * s->attn.H;
   CSA_SUPPORTED(R <= 0x7fffffffLL - 128);
@@ -771,7 +772,7 @@ static csa_status run_shared(const csa_shared_attn_args* s, void* ws, size_t ws_
   const int slots = p.own + p.pslots;
   csa_status r = CSA_OK;
   if (p.own > 0) r = launch_attn_tc(a, 1, s->n_prefix, p.own, slots, p.tpc, po, pl, st);
-  if (r == CSA_OK) r = launch_attn_prefix(a, s->prefix_kv, s->n_prefix, p.ctas, p.own, p.pslots, slots, po, pl, st);
+  if (r == CSA_OK) r = launch_attn_prefix(a, s->prefix_kv, s->n_prefix, p.pairs, p.own, p.pslots, slots, po, pl, st);
   if (r != CSA_OK) return r;
   return launch_merge<uint16_t>(po, pl, slots, a->H, a->d, rows, (uint16_t*)a->out, a->lse, a->q_pos, a->out_rope_theta, st);
 }

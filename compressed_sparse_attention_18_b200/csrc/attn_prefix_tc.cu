@@ -1,23 +1,30 @@
 // HCA attention over a prefix of compressed entries that every sequence of the batch shares, on the 5th-generation
 // tensor cores: the partial softmax attention of all query rows (each a head of a query) over the prefix's bf16 rows.
-// Since the prefix is the same for all and there is one shared KV head, the rows of the whole batch form one matrix,
-// and a CTA attends with 96 of them at a time over tiles of 128 entries:
+// Since the prefix is the same for all and there is one shared KV head, the rows of the whole batch form one matrix;
+// a pair of CTAs attends with 128 of them at a time over tiles of 256 entries (K = V, 512 wide):
 //
-//   S^T[key][row] = K[key][:] . Q[row][:]          M = 128 keys, N = 96 rows, K = 512 (32 MMAs, K-major)
-//   P^T = exp2(S^T * scale*log2e - m_row)          m: a running reference per row, see below
-//   O^T[dim][row] += sum_key K[key][dim] P^T[key][row]   M = 4 x 128 dims, N = 96, K = 128 (32 MMAs, both MN-major)
+//   S[row][key] = Q[row][:] . K[key][:]              M = 128 rows, N = 256 keys, K = 512 (32 MMAs)
+//   P = exp2(S * scale*log2e - m_row)                m: a running reference per row, see below
+//   O[row][dim] += sum_key P[row][key] K[key][dim]   M = 128, N = 2 x 256 dims, K = 256 (32 MMAs)
 //
-// The per-query kernels dequantise every entry again for every query and reach an N of 64; here entries arrive as
-// bf16 by TMA and N = 96 costs no more than 64: an M = 128 bf16 MMA takes 59 cycles at N = 64 and at N = 96 (64 at 128,
-// measured), so 96 rows run at 6650 of the 8190 flop a cycle and SM.  O^T takes 4 x 96 columns of tensor memory, S^T 96.
+// What bounds it is shared memory: an SM reads 128 bytes a cycle, and 16-deep MMAs that keep both operands there need
+// 7 KB for 128 x 96 (one CTA, entries as the 128 rows: 8560 cycles a tile of 128 keys x 96 rows were measured, 2940
+// flop a cycle) but 6 KB for 64 x 256 an SM here: with cta_group::2 each CTA holds 64 rows of A and half of B, and M = 128
+// over a pair runs at the full rate from N = 256 on (64 cycles, measured).  O takes 256 columns of tensor memory, S 128:
+// a CTA's lanes 0-63 hold its 64 rows over the first half of N, lanes 64-127 the same rows over the second half.
 //
-// Shared memory: Q (96 KB) stays; the 8 chunks (128 keys x 64 dims, 16 KB) of a tile pass through a ring of 6.  S needs
-// chunks 0..7, then O takes 2 3 | 4 5 | 6 7, which are still there, and 0 1, which come a second time: 10 loads a tile.
-// Softmax: the reference m of a row moves only when a tile's scores exceed it by more than 2^8 (or in a part's first
-// tile), which the threads of a column group agree on with one barrier; the sum stays in registers, one partial sum
-// per thread and row, until the part ends.
-// Parts: the tiles of all blocks of 96 rows form one line that is cut evenly over the CTAs, so a CTA works on the
-// end of one block and the start of the next, and each leaves a partial (O / l in bf16, lse) that the split merge adds.
+// Operands: S wants from CTA c the tile's keys 128 c .. 128 c + 127 over all dims (8 chunks of 128 keys x 64 dims,
+// 16 KB), O wants all 256 keys over the dims 128 c .. and 256 + 128 c ..  Half of the chunks serve both; the others
+// are replaced in place once S has read them (12 loads a tile instead of 16):
+//   slot        0    1    2    3    4    5    6    7
+//   S  (c)    dims 64 j .. of keys 128 c ..
+//   O  (0)    kept kept new  new  kept kept new  new     (keys 0 .. in slots 0 1 4 5, keys 128 .. in 2 3 6 7;
+//   O  (1)    new  new  kept kept new  new  kept kept     dims 128 c + 64 (j & 1) .. in 0-3, 256 more in 4-7)
+// Softmax: a row's reference m moves only when a tile's scores exceed it by more than 2^8 (or in a part's first tile),
+// which the CTA's threads agree on with one barrier; a thread sums its own columns until the part ends.
+// Parts: the tiles of all blocks of 128 rows form one line that is cut evenly over the pairs, so a pair works on the end
+// of one block and the start of the next, and each leaves a partial (O / l in bf16, lse) that the split merge adds.
+// Every wait is bounded; a wait that gives up records device error 1 and the kernel leaves.
 // Sources: "DeepSeek-V4: エージェントが実際に使える100万トークンのコンテキスト", §ハイブリッド注意, Fig. 4 (the 128x layer
 // attends densely over all visible entries).
 #include "csa_common.cuh"
@@ -27,24 +34,25 @@ namespace csa {
 
 using namespace sm100;
 
-constexpr int PX_COLS = 96;                 // query rows of a block
-constexpr int PX_KEYS = 128;
-constexpr int PX_WORKERS = 384;             // warps 0-11: 4 lane quadrants (keys, dims) x 3 groups of 32 rows
-constexpr int PX_THREADS = PX_WORKERS + 64; // warp 12: TMA, warp 13: tensor memory and MMA
-constexpr int PX_SLOTS = 6, PX_CHUNK = PX_KEYS * 128, PX_LOADS = 10;
-constexpr uint32_t PX_COL_S = 0, PX_COL_O = 96;
+constexpr int PX_ROWS = 128;                // query rows of a block: 64 a CTA
+constexpr int PX_KEYS = 256;                // entries of a tile
+constexpr int PX_WORKERS = 256;             // warps 0-7: 4 lane quadrants x 2 halves of a lane's columns
+constexpr int PX_THREADS = PX_WORKERS + 64; // warp 8: TMA, warp 9: tensor memory, MMA (rank 0)
+constexpr int PX_CHUNK = 128 * 128;         // 128 keys x 64 dims bf16
+constexpr uint32_t PX_COL_S = 0, PX_COL_O = 128;
 constexpr float PX_SLACK = 8.0f;            // log2 units: probabilities stay <= 2^8
 constexpr float PX_LOG2E = 1.4426950408889634f, PX_LN2 = 0.6931471805599453f;
 
 struct PxSmem {
-  alignas(1024) uint8_t Q[8][PX_COLS * 128];     // [dim block][row][128 B], 128-byte swizzle
-  alignas(1024) uint8_t K[PX_SLOTS][PX_CHUNK];   // [key][128 B], 128-byte swizzle
-  alignas(1024) uint8_t P[3][PX_KEYS * 64];      // [group][key][32 rows bf16], 64-byte swizzle
-  alignas(16) float m[PX_COLS];                  // reference (log2 units); 0 for a row that sees no key
-  alignas(16) float inv[PX_COLS];                // 1 / l at a part's end
-  float red[4][PX_COLS];
-  alignas(8) uint64_t full[PX_SLOTS], rel[PX_SLOTS];
-  uint64_t bar_q, bar_qfree, bar_s, bar_p, bar_o;
+  alignas(1024) uint8_t Q[8][64 * 128];     // [dim block][row][128 B], 128-byte swizzle
+  alignas(1024) uint8_t K[8][PX_CHUNK];     // [slot][key][128 B], 128-byte swizzle
+  alignas(1024) uint8_t P[4][64 * 128];     // [64 keys][row][128 B], 128-byte swizzle
+  float red[4][64];                         // [key quarter][row]
+  alignas(8) uint64_t full[8];              // rank 0: a slot's operands have landed in both CTAs (twice a tile: S, O)
+  uint64_t rel[8];                          // both: a slot has been read (twice a tile: by S, by O)
+  uint64_t bar_q;                           // rank 0: Q has landed in both
+  uint64_t bar_qfree, bar_s, bar_o;         // both: Q read; S complete; O complete
+  uint64_t bar_p;                           // rank 0: P written (and S read) in both
   uint32_t tmem_base;
   uint32_t err;
 };
@@ -52,7 +60,7 @@ struct PxSmem {
 struct PxParams {
   long long R;            // query rows: B * Nq * H
   long long T;            // tiles of all blocks
-  int tiles;              // tiles of one block: ceil(n_p / 128)
+  int tiles;              // tiles of one block: ceil(n_p / 256)
   int Nq, H, ratio, n_p, n_max;
   int slot0, slots;       // partial slots of a query: this kernel's first, and all
   int pslots;             // this kernel's
@@ -63,339 +71,315 @@ struct PxParams {
   float* part_lse;        // [query][slots][H]
 };
 
-// The CTA that tile g of the line belongs to when it is cut into G even parts [i T / G, (i + 1) T / G).
-__host__ __device__ __forceinline__ long long px_cta_of(long long g, long long G, long long T) { return ((g + 1) * G - 1) / T; }
+// The pair that tile g of the line belongs to when it is cut into G even parts [i T / G, (i + 1) T / G).
+__host__ __device__ __forceinline__ long long px_pair_of(long long g, long long G, long long T) { return ((g + 1) * G - 1) / T; }
 
 __device__ __forceinline__ float px_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ void px_group_sync(int g) { asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory"); }
-// Barrier of a column group that returns whether any of its threads passed true.
-__device__ __forceinline__ bool px_group_any(int g, bool v) {
+__device__ __forceinline__ void px_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+// Barrier of the softmax warps that returns whether any of their threads passed true.
+__device__ __forceinline__ bool px_any(bool v) {
   uint32_t r;
   asm volatile(
-      "{ .reg .pred p, q; setp.ne.b32 p, %2, 0; barrier.cta.red.or.pred q, %1, 128, p; selp.u32 %0, 1, 0, q; }"
-      : "=r"(r) : "r"(1 + g), "r"((uint32_t)v) : "memory");
+      "{ .reg .pred p, q; setp.ne.b32 p, %1, 0; barrier.cta.red.or.pred q, 1, 256, p; selp.u32 %0, 1, 0, q; }"
+      : "=r"(r) : "r"((uint32_t)v) : "memory");
   return r != 0;
 }
-// 32 values per lane reduced over the warp's lanes, transposed: lane l returns the reduction of value l.
-template <bool kMax>
-__device__ __forceinline__ float px_transpose_reduce(float (&v)[32], int lane) {
-#pragma unroll
-  for (int s = 16; s >= 1; s >>= 1) {
-    const bool up = (lane & s) != 0;
-#pragma unroll
-    for (int i = 0; i < s; ++i) {
-      const float send = up ? v[i] : v[i + s], keep = up ? v[i + s] : v[i];
-      const float got = __shfl_xor_sync(0xffffffffu, send, s);
-      v[i] = kMax ? fmaxf(keep, got) : keep + got;
-    }
-  }
-  return v[0];
-}
-__device__ __forceinline__ void px_tmem_st_x32(uint32_t taddr, const uint32_t* r) {
-  tmem_st_x16(taddr, r);
-  tmem_st_x16(taddr + 16, r + 16);
-}
 
-__global__ void __launch_bounds__(PX_THREADS, 1)
+__global__ void __launch_bounds__(PX_THREADS, 1) __cluster_dims__(2, 1, 1)
     attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                           const PxParams P) {
   extern __shared__ uint8_t smem_raw[];
   PxSmem& S = *reinterpret_cast<PxSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const long long G = gridDim.x, g_begin = blockIdx.x * P.T / G, g_end = (blockIdx.x + 1) * P.T / G;
+  const int rank = (int)blockIdx.x & 1;
+  const long long pair = blockIdx.x >> 1, G = gridDim.x >> 1;
+  const long long g_begin = pair * P.T / G, g_end = (pair + 1) * P.T / G;
   if (tid == 0) {
     S.err = 0;
-    for (int i = 0; i < PX_SLOTS; ++i) { mbar_init(&S.full[i], 1); mbar_init(&S.rel[i], 1); }
+    for (int i = 0; i < 8; ++i) { mbar_init(&S.full[i], 1); mbar_init(&S.rel[i], 1); }
     mbar_init(&S.bar_q, 1);
     mbar_init(&S.bar_qfree, 1);
     mbar_init(&S.bar_s, 1);
-    mbar_init(&S.bar_p, PX_WORKERS / 32);
     mbar_init(&S.bar_o, 1);
+    mbar_init(&S.bar_p, 2 * PX_WORKERS / 32);
     fence_mbar_init();
     prefetch_tensormap(&qmap);
     prefetch_tensormap(&kmap);
   }
-  if (warp == 13) { tmem_alloc(&S.tmem_base, 512); tmem_relinquish(); }
+  if (warp == 9) { tmem_alloc_pair(&S.tmem_base, 512); tmem_relinquish_pair(); }
   pdl_trigger();
   __syncthreads();
+  cluster_sync_all();                        // both CTAs' barriers and tensor memory are there
   tc_fence_after();
   const uint32_t tb = S.tmem_base;
   bool ok = true;
   pdl_wait();
 
-  if (warp == 12) {
-    // ------------------------------------------------------------------------ TMA producer
+  if (warp == 8) {
+    // ------------------------------------------------------------------------ TMA producer (one per CTA)
     if (lane == 0) {
-      uint32_t n = 0, part = 0;
+      uint32_t tile = 0, part = 0;
       for (long long g = g_begin; g < g_end && ok; ++part) {
         const long long blk = g / P.tiles, blk_end = (blk + 1) * P.tiles, e = blk_end < g_end ? blk_end : g_end;
         // the previous part's S MMAs have read Q
         if (part > 0 && !mbar_wait(&S.bar_qfree, (part - 1) & 1)) { ok = false; break; }
-        mbar_arrive_expect_tx(&S.bar_q, 8 * PX_COLS * 128);
-        for (int j = 0; j < 8; ++j) tma_load_2d(S.Q[j], &qmap, j * 64, (int)(blk * PX_COLS), &S.bar_q);
-        for (; g < e && ok; ++g) {
+        if (rank == 0) mbar_arrive_expect_tx(&S.bar_q, 2 * 8 * 64 * 128);
+        for (int j = 0; j < 8; ++j)
+          tma_load_2d_pair(S.Q[j], &qmap, j * 64, (int)(blk * PX_ROWS) + 64 * rank, peer_addr(&S.bar_q, 0));
+        for (; g < e && ok; ++g, ++tile) {
           const int key0 = (int)(g - blk * P.tiles) * PX_KEYS;
-          for (int k = 0; k < PX_LOADS; ++k, ++n) {
-            const uint32_t s = n % PX_SLOTS, f = n / PX_SLOTS;
-            if (f > 0 && !mbar_wait(&S.rel[s], (f - 1) & 1)) { ok = false; break; }
-            mbar_arrive_expect_tx(&S.full[s], PX_CHUNK);
-            tma_load_2d(S.K[s], &kmap, (k & 7) * 64, key0, &S.full[s]);
+          for (int j = 0; j < 8 && ok; ++j) {
+            if (tile > 0 && !mbar_wait(&S.rel[j], 1)) { ok = false; break; }      // read by the previous tile's O
+            if (rank == 0) mbar_arrive_expect_tx(&S.full[j], 2 * PX_CHUNK);
+            tma_load_2d_pair(S.K[j], &kmap, j * 64, key0 + 128 * rank, peer_addr(&S.full[j], 0));
+          }
+          for (int j = 0; j < 8 && ok; ++j) {
+            if (!mbar_wait(&S.rel[j], 0)) { ok = false; break; }                  // read by S
+            const int owner = (j & 2) ? 0 : 1;                                    // whose chunk is not the one O wants
+            if (rank == 0) mbar_arrive_expect_tx(&S.full[j], PX_CHUNK);
+            if (rank == owner)
+              tma_load_2d_pair(S.K[j], &kmap, ((j & 4) ? 256 : 0) + 128 * rank + 64 * (j & 1), key0 + ((j & 2) ? 128 : 0),
+                               peer_addr(&S.full[j], 0));
           }
         }
       }
       if (!ok) {
         atomicOr(&S.err, 1u);
-        // drain: the copies this thread issued complete before the CTA may leave
-        for (uint32_t i = n > PX_SLOTS ? n - PX_SLOTS : 0; i < n; ++i)
-          mbar_wait(&S.full[i % PX_SLOTS], (i / PX_SLOTS) & 1, 1u << 16);
+        for (int i = 0; i < 1000; ++i) __nanosleep(200);       // copies in flight land before the CTA may leave
       }
     }
     __syncwarp();
-  } else if (warp == 13) {
+  } else if (warp == 9) {
     // ------------------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      const uint32_t ids = idesc_bf16(128, PX_COLS, 0, 0), ido = idesc_bf16(128, PX_COLS, 1, 1);
-      const uint64_t kdesc = smem_desc(smem_addr(S.K[0]), 16, 1024, LAYOUT_SW128);
+    // (the whole warp of rank 0 walks, one lane issues: see elect_one)
+    if (rank == 0) {
+      const uint32_t ids = idesc_bf16(128, 256, 0, 0), ido = idesc_bf16(128, 256, 0, 1);
       const uint64_t qdesc = smem_desc(smem_addr(S.Q[0]), 16, 1024, LAYOUT_SW128);
+      const uint64_t kdesc = smem_desc(smem_addr(S.K[0]), 16, 1024, LAYOUT_SW128);
       const uint64_t vdesc = smem_desc(smem_addr(S.K[0]), PX_CHUNK, 1024, LAYOUT_SW128);
-      const uint64_t pdesc = smem_desc(smem_addr(S.P[0]), PX_KEYS * 64, 512, LAYOUT_SW64);
-      uint32_t n0 = 0, f = 0, part = 0;
-      auto chunk_ready = [&](uint32_t n) {
-        uint64_t* bar = &S.full[n % PX_SLOTS];
-        const uint32_t ph = (n / PX_SLOTS) & 1;
+      const uint64_t pdesc = smem_desc(smem_addr(S.P[0]), 16, 1024, LAYOUT_SW128);
+      auto landed = [&](uint64_t* bar, uint32_t ph) {
         if (!mbar_test(bar, ph)) ok = ok && mbar_wait(bar, ph);
       };
+      uint32_t f = 0, part = 0;
       for (long long g = g_begin; g < g_end && ok; ++part) {
         const long long blk_end = (g / P.tiles + 1) * P.tiles, e = blk_end < g_end ? blk_end : g_end;
         ok = mbar_wait(&S.bar_q, part & 1);
-        for (long long t = g; t < e && ok; ++t, ++f, n0 += PX_LOADS) {
-          // S^T = K Q^T, chunk by chunk as they land
+        const int n = (int)(e - g);
+#pragma unroll 1
+        for (int t = 0; t < n && ok; ++t, ++f) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            chunk_ready(n0 + j);
-            if (!ok) continue;
+            landed(&S.full[j], 0);
             tc_fence_after();
-            const uint32_t s = (n0 + j) % PX_SLOTS;
+            if (elect_one()) {
 #pragma unroll
-            for (int s2 = 0; s2 < 4; ++s2)
-              mma_bf16_ss(tb + PX_COL_S, kdesc + (uint64_t)((s * PX_CHUNK + s2 * 32) >> 4),
-                          qdesc + (uint64_t)((j * PX_COLS * 128 + s2 * 32) >> 4), ids, (j | s2) != 0);
-            if (j < 2) mma_commit(&S.rel[s]);        // chunks 0 and 1 come again for O
+              for (int s = 0; s < 4; ++s)
+                mma_bf16_ss_pair(tb + PX_COL_S, qdesc + (uint64_t)((j * 64 * 128 + s * 32) >> 4),
+                                 kdesc + (uint64_t)((j * PX_CHUNK + s * 32) >> 4), ids, (j | s) != 0);
+              mma_commit_pair(&S.rel[j]);
+              if (j == 7) {
+                mma_commit_pair(&S.bar_s);
+                if (t + 1 == n) mma_commit_pair(&S.bar_qfree);
+              }
+            }
+            __syncwarp();
           }
-          mma_commit(&S.bar_s);
-          if (t + 1 == e) mma_commit(&S.bar_qfree);
           ok = ok && mbar_wait(&S.bar_p, f & 1);
-          if (ok) tc_fence_after();
-          // O^T += V^T P^T: dims 128.., 256.., 384.. from the chunks that stayed, then 0..
+          tc_fence_after();
+          // slots 2 i, 2 i + 1: keys 128 (i & 1) .., dims 256 (i >> 1) ..
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int mt = (i + 1) & 3;
-            const uint32_t n = n0 + (mt ? 2 * mt : 8), s = n % PX_SLOTS;
-            if (mt == 0) { chunk_ready(n); chunk_ready(n + 1); }
-            if (!ok) continue;
+            landed(&S.full[2 * i], 1);
+            landed(&S.full[2 * i + 1], 1);
             tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
-            for (int s2 = 0; s2 < 8; ++s2)
-              mma_bf16_ss(tb + PX_COL_O + PX_COLS * mt, vdesc + (uint64_t)((s * PX_CHUNK + s2 * 2048) >> 4),
-                          pdesc + (uint64_t)((s2 * 1024) >> 4), ido, t > g || s2 > 0);
-            mma_commit(&S.rel[s]);
-            mma_commit(&S.rel[s + 1]);
+              for (int s = 0; s < 8; ++s)
+                mma_bf16_ss_pair(tb + PX_COL_O + 128 * (i >> 1),
+                                 pdesc + (uint64_t)(((2 * (i & 1) + (s >> 2)) * 64 * 128 + (s & 3) * 32) >> 4),
+                                 vdesc + (uint64_t)((2 * i * PX_CHUNK + s * 2048) >> 4), ido, t > 0 || (i & 1) || s > 0);
+              mma_commit_pair(&S.rel[2 * i]);
+              mma_commit_pair(&S.rel[2 * i + 1]);
+              if (i == 3 && t + 1 == n) mma_commit_pair(&S.bar_o);
+            }
+            __syncwarp();
           }
-          if (t + 1 == e) mma_commit(&S.bar_o);
         }
         g = e;
       }
-      if (!ok) atomicOr(&S.err, 1u);
+      if (!ok && lane == 0) atomicOr(&S.err, 1u);
     }
     __syncwarp();
   } else {
     // ------------------------------------------------------------------------ softmax and epilogue
-    const int quad = warp & 3, grp = warp >> 2;
-    const int kr = 32 * quad + lane;             // the thread's key of a tile, and its dim of 128 in the epilogue
-    const uint32_t lane_base = tb + ((uint32_t)(32 * quad) << 16) + 32 * grp;
-    uint8_t* prow = &S.P[grp][kr * 64];
-    const float4* m4 = reinterpret_cast<const float4*>(&S.m[32 * grp]);
+    // warp: lane quadrant `quad`, columns 64 ch .. of its lanes.  A thread has one row, and of a tile the 64 keys
+    // of quarter kq; of O the dims 128 (quad >> 1) .. of each 256.
+    const int quad = warp & 3, ch = warp >> 2;
+    const int row = 32 * (quad & 1) + lane, kq = 2 * (quad >> 1) + ch;
+    const uint32_t lane_base = tb + ((uint32_t)(32 * quad) << 16);
+    uint8_t* prow = &S.P[kq][row * 128];
+    const uint32_t bar_p = peer_addr(&S.bar_p, 0);
     uint32_t f = 0, part = 0;
     for (long long g = g_begin; g < g_end; ++part) {
       const long long blk = g / P.tiles, blk_end = (blk + 1) * P.tiles, e = blk_end < g_end ? blk_end : g_end;
-      // lane l of every warp speaks for row l of its group: how many entries it sees (rows behind the last
-      // query row see all of them: their Q is zero and nothing is stored), its reference, its partial's place
-      const long long col = blk * PX_COLS + 32 * grp + lane;
-      const bool real = col < P.R;
+      // how many entries the row sees (rows behind the last query row: all of them, their Q is zero and nothing is
+      // stored), and its place in the partials without the slot
+      const long long qr = blk * PX_ROWS + 64 * rank + row;
+      const bool real = qr < P.R;
       int nv = P.n_p;
-      long long prt = 0;                         // row of the partial arrays, without the slot
+      long long prt = 0;
       if (real) {
-        const long long bq = col / P.H;
+        const long long bq = qr / P.H;
         const int b = (int)(bq / P.Nq);
         const long long see = (P.q_pos[bq] + 1) / P.ratio;
         nv = (int)max(0LL, min((long long)min(P.n_p, min(P.n_c[b], P.n_max)), see));
-        prt = bq * P.slots * P.H + (col - bq * P.H);
+        prt = bq * P.slots * P.H + (qr - bq * P.H);
       }
-      int nv_min = nv;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) nv_min = min(nv_min, __shfl_xor_sync(0xffffffffu, nv_min, o));
-      float m_l = -INFINITY;
-      float l[32];
-#pragma unroll
-      for (int j = 0; j < 32; ++j) l[j] = 0.f;
+      float m = -INFINITY;                       // the row's reference (log2 units); its four threads agree
+      float l = 0.f;                             // this thread's part of the row's sum
       for (long long t = g; t < e; ++t, ++f) {
         const bool first = t == g;
-        const int key0 = (int)(t - blk * P.tiles) * PX_KEYS;
+        // keys of this thread that the row sees
+        const int lim = nv - ((int)(t - blk * P.tiles) * PX_KEYS + 64 * kq);
         ok = ok && mbar_wait(&S.bar_s, f & 1);
         tc_fence_after();
-        float z[32];
+        float z[64];
         {
-          uint32_t v[32];
-          tmem_ld_x32(lane_base + PX_COL_S, v);
+          uint32_t v[32], w[32];
+          tmem_ld_x32(lane_base + PX_COL_S + 64 * ch, v);
+          tmem_ld_x32(lane_base + PX_COL_S + 64 * ch + 32, w);
           tmem_wait_ld_x32(v);
+          tmem_wait_ld_x32(w);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) z[j] = __uint_as_float(v[j]);
+          for (int j = 0; j < 32; ++j) { z[j] = __uint_as_float(v[j]); z[j + 32] = __uint_as_float(w[j]); }
         }
-        if (key0 + PX_KEYS > nv_min) {           // some row of the group does not see the whole tile
+        if (lim < 64) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (key0 + kr >= __shfl_sync(0xffffffffu, nv, j)) z[j] = -INFINITY;
+          for (int j = 0; j < 64; ++j)
+            if (j >= lim) z[j] = -INFINITY;
         }
-        bool move = first;
-        if (!first) {
-          float top = -INFINITY;
+        float top = z[0];
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            const float4 mm = m4[j >> 2];
-            top = fmaxf(top, fmaxf(fmaxf(fmaf(z[j], P.scale_log2, -mm.x), fmaf(z[j + 1], P.scale_log2, -mm.y)),
-                                   fmaxf(fmaf(z[j + 2], P.scale_log2, -mm.z), fmaf(z[j + 3], P.scale_log2, -mm.w))));
-          }
-          move = px_group_any(grp, top > PX_SLACK);
-        }
-        if (move) {
-          float v[32];
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = z[j] * P.scale_log2;
-          S.red[quad][32 * grp + lane] = px_transpose_reduce<true>(v, lane);
-          px_group_sync(grp);
-          const int c = 32 * grp + lane;
-          const float mt = fmaxf(fmaxf(S.red[0][c], S.red[1][c]), fmaxf(S.red[2][c], S.red[3][c]));
-          const float mn = first || mt > m_l + PX_SLACK ? fmaxf(m_l, mt) : m_l;
-          const float fc = first || mn == m_l ? 1.f : exp2f(m_l - mn);
-          m_l = mn;
-          if (quad == 0) S.m[c] = mn == -INFINITY ? 0.f : mn;
-          px_group_sync(grp);
+        for (int j = 1; j < 64; ++j) top = fmaxf(top, z[j]);
+        top *= P.scale_log2;                     // (the scale is positive)
+        if (first || px_any(top > m + PX_SLACK)) {
+          S.red[kq][row] = top;
+          px_sync();
+          const float mt = fmaxf(fmaxf(S.red[0][row], S.red[1][row]), fmaxf(S.red[2][row], S.red[3][row]));
+          const float mn = first || mt > m + PX_SLACK ? fmaxf(m, mt) : m;
+          const float fc = first || mn == m ? 1.f : exp2f(m - mn);
+          m = mn;
+          l *= fc;
           if (!first && __any_sync(0xffffffffu, fc != 1.f)) {
-            // the sums and O^T of the rows whose reference moved (the O MMAs so far completed before S did)
-#pragma unroll
-            for (int j = 0; j < 32; ++j) l[j] *= __shfl_sync(0xffffffffu, fc, j);
+            // O of the rows whose reference moved (the O MMAs so far completed before S did); this thread's half of
+            // its lane's 256 columns
 #pragma unroll 1
-            for (int mt4 = 0; mt4 < 4; ++mt4) {
+            for (int c = 0; c < 4; ++c) {
               uint32_t o[32];
-              const uint32_t at = lane_base + PX_COL_O + PX_COLS * mt4;
+              const uint32_t at = lane_base + PX_COL_O + 128 * ch + 32 * c;
               tmem_ld_x32(at, o);
               tmem_wait_ld_x32(o);
 #pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * __shfl_sync(0xffffffffu, fc, j));
-              px_tmem_st_x32(at, o);
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * fc);
+              tmem_st_x16(at, o);
+              tmem_st_x16(at + 16, o + 16);
             }
             tmem_wait_st();
           }
+          px_sync();                             // red has been read
         }
+        const float mm = m == -INFINITY ? 0.f : m;   // (a row that sees no key: every z is -inf)
 #pragma unroll
-        for (int j = 0; j < 32; j += 8) {
-          const float4 ma = m4[j >> 2], mb = m4[(j >> 2) + 1];
-          const float mm[8] = {ma.x, ma.y, ma.z, ma.w, mb.x, mb.y, mb.z, mb.w};
+        for (int j = 0; j < 64; j += 8) {
           float p[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            p[i] = px_exp2(fmaf(z[j + i], P.scale_log2, -mm[i]));
-            l[j + i] += p[i];
+            p[i] = px_exp2(fmaf(z[j + i], P.scale_log2, -mm));
+            l += p[i];
           }
           // P is rounded to bf16 for the MMA (2^-8 of a probability); l adds the unrounded values
-          *reinterpret_cast<uint4*>(prow + ((((j >> 3) ^ (kr >> 1)) & 3) << 4)) =
+          *reinterpret_cast<uint4*>(prow + ((((j >> 3) ^ row) & 7) << 4)) =
               make_uint4(pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]), pack_bf16x2(p[4], p[5]), pack_bf16x2(p[6], p[7]));
         }
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&S.bar_p);
+        if (lane == 0) mbar_arrive_cluster(bar_p);
       }
-      // ---- the part's partial: O^T / l, lane = dim, columns = rows
-      const long long first_cta = px_cta_of(blk * P.tiles, G, P.T);
-      const int slot = P.slot0 + (int)(blockIdx.x - first_cta);
-      S.red[quad][32 * grp + lane] = px_transpose_reduce<false>(l, lane);
-      px_group_sync(grp);
-      {
-        const int c = 32 * grp + lane;
-        const float lt = (S.red[0][c] + S.red[1][c]) + (S.red[2][c] + S.red[3][c]);
-        if (quad == 0) {
-          S.inv[c] = lt > 0.f ? 1.f / lt : (lt == 0.f ? 0.f : lt);       // (a NaN stays one)
-          if (real) {
-            P.part_lse[prt + (long long)slot * P.H] = lt == 0.f ? -INFINITY : (m_l + log2f(lt)) * PX_LN2;
-            // slots of this block that no CTA fills
-            if (e == blk_end)
-              for (int s = slot + 1; s < P.slot0 + P.pslots; ++s) P.part_lse[prt + (long long)s * P.H] = -INFINITY;
-          }
-        }
+      // ---- the part's partial: O / l
+      const int slot = P.slot0 + (int)(pair - px_pair_of(blk * P.tiles, G, P.T));
+      const long long out = prt + (long long)slot * P.H;
+      S.red[kq][row] = l;
+      px_sync();
+      const float lt = (S.red[0][row] + S.red[1][row]) + (S.red[2][row] + S.red[3][row]);
+      px_sync();                                 // red is free again
+      const float inv = lt == 0.f ? 0.f : 1.f / lt;
+      if (real && kq == 0) {
+        P.part_lse[out] = lt == 0.f ? -INFINITY : (m + log2f(lt)) * PX_LN2;
+        // slots of this block that no pair fills
+        if (e == blk_end)
+          for (int s = slot + 1; s < P.slot0 + P.pslots; ++s) P.part_lse[prt + (long long)s * P.H] = -INFINITY;
       }
-      px_group_sync(grp);
       ok = ok && mbar_wait(&S.bar_o, part & 1);
       tc_fence_after();
-      const float4* i4 = reinterpret_cast<const float4*>(&S.inv[32 * grp]);
-      const int n_real = (int)min(32LL, P.R - (blk * PX_COLS + 32 * grp));
-      const long long row = prt + (long long)slot * P.H;
+      // columns 128 ch ..: dims 256 ch + 128 (quad >> 1) ..
+      uint16_t* dst = P.part_o + out * 512 + 256 * ch + 128 * (quad >> 1);
 #pragma unroll 1
-      for (int mt = 0; mt < 4; ++mt) {
+      for (int c = 0; c < 4; ++c) {
         uint32_t o[32];
-        tmem_ld_x32(lane_base + PX_COL_O + PX_COLS * mt, o);
+        tmem_ld_x32(lane_base + PX_COL_O + 128 * ch + 32 * c, o);
         tmem_wait_ld_x32(o);
+        if (real)
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          const float4 iv = i4[j >> 2];
-          const float f4[4] = {iv.x, iv.y, iv.z, iv.w};
+          for (int j = 0; j < 32; j += 8) {
+            uint32_t w[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const long long r = __shfl_sync(0xffffffffu, row, j + i);
-            if (j + i < n_real)
-              P.part_o[r * 512 + 128 * mt + kr] = (uint16_t)f_to_bf16_bits(__uint_as_float(o[j + i]) * f4[i]);
+            for (int i = 0; i < 4; ++i)
+              w[i] = pack_bf16x2(__uint_as_float(o[j + 2 * i]) * inv, __uint_as_float(o[j + 2 * i + 1]) * inv);
+            *reinterpret_cast<uint4*>(dst + 32 * c + j) = make_uint4(w[0], w[1], w[2], w[3]);
           }
-        }
       }
       tc_fence_before();
-      // the group's red and inv are rewritten only after all of its warps have read them
-      px_group_sync(grp);
       g = e;
     }
     if (!ok && lane == 0) atomicOr(&S.err, 1u);
   }
+  // every MMA has completed (the last part's O was waited for in both CTAs) and no arrival is on its way to a CTA
+  // that has left
   __syncthreads();
-  if (warp == 13) {
-    if (S.err && lane == 0) atomicOr(&g_csa_device_error, 1u);
+  if (S.err && tid == 0) atomicOr(&g_csa_device_error, 1u);
+  cluster_sync_all();
+  if (warp == 9) {
     tc_fence_after();
-    tmem_dealloc(tb, 512);
+    tmem_dealloc_pair(tb, 512);
   }
 }
 
-// The prefix kernel's plan for R query rows over n_p entries: CTAs, and partial slots a query needs (at most `most`).
-void attn_prefix_plan(long long R, int n_p, int most, int* ctas, int* slots) {
-  const long long blocks = (R + PX_COLS - 1) / PX_COLS, tiles = ((long long)n_p + PX_KEYS - 1) / PX_KEYS, T = blocks * tiles;
-  long long G = T < 148 ? T : 148;
+// The prefix kernel's plan for R query rows over n_p entries: pairs of CTAs, and partial slots a query needs (at most
+// `most`).
+void attn_prefix_plan(long long R, int n_p, int most, int* pairs, int* slots) {
+  const long long blocks = (R + PX_ROWS - 1) / PX_ROWS, tiles = ((long long)n_p + PX_KEYS - 1) / PX_KEYS, T = blocks * tiles;
+  long long G = T < 74 ? T : 74;
   if (G > blocks * (most - 1)) G = blocks * (most - 1);    // a block is cut into at most ceil(G / blocks) + 1 parts
   long long worst = 1;
-  // (with no fewer blocks than CTAs every part is at least a block's worth: two CTAs a block at most)
   if (blocks >= G) {
-    worst = blocks == G ? 1 : 2;
+    worst = blocks == G ? 1 : 2;                           // every part is at least a block's worth
   } else {
     for (long long b = 0; b < blocks; ++b) {
-      const long long n = px_cta_of((b + 1) * tiles - 1, G, T) - px_cta_of(b * tiles, G, T) + 1;
+      const long long n = px_pair_of((b + 1) * tiles - 1, G, T) - px_pair_of(b * tiles, G, T) + 1;
       if (n > worst) worst = n;
     }
   }
-  *ctas = (int)G;
+  *pairs = (int)G;
   *slots = (int)worst;
 }
 
-csa_status launch_attn_prefix(const csa_attn_args* a, const void* prefix, int n_p, int ctas, int slot0, int pslots, int slots,
+csa_status launch_attn_prefix(const csa_attn_args* a, const void* prefix, int n_p, int pairs, int slot0, int pslots, int slots,
                               uint16_t* part_o, float* part_lse, cudaStream_t st) {
   const long long R = (long long)a->B * a->Nq * a->H;
   CUtensorMap qm, km;
@@ -408,19 +392,20 @@ csa_status launch_attn_prefix(const csa_attn_args* a, const void* prefix, int n_
                                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   };
-  if (!encode(&qm, a->q, R, PX_COLS) || !encode(&km, prefix, n_p, PX_KEYS)) return CSA_ERR_CUDA;
+  if (!encode(&qm, a->q, R, 64) || !encode(&km, prefix, n_p, 128)) return CSA_ERR_CUDA;
   PxParams P{};
   P.R = R;
   P.tiles = (n_p + PX_KEYS - 1) / PX_KEYS;
-  P.T = (R + PX_COLS - 1) / PX_COLS * P.tiles;
+  P.T = (R + PX_ROWS - 1) / PX_ROWS * P.tiles;
   P.Nq = a->Nq; P.H = a->H; P.ratio = a->ratio; P.n_p = n_p; P.n_max = a->n_max;
   P.slot0 = slot0; P.slots = slots; P.pslots = pslots;
   P.scale_log2 = (a->softmax_scale != 0.0f ? a->softmax_scale : 1.0f / sqrtf(512.0f)) * PX_LOG2E;
   P.q_pos = a->q_pos; P.n_c = a->n_c; P.part_o = part_o; P.part_lse = part_lse;
   const int smem = (int)sizeof(PxSmem) + 1024;
+  static_assert(sizeof(PxSmem) + 1024 <= 232448, "shared memory of a CTA");
   static std::atomic<unsigned> attr_done{0};
   set_smem_once((const void*)attn_prefix_tc_kernel, smem, attr_done);
-  return launch_pdl(attn_prefix_tc_kernel, dim3((unsigned)ctas), dim3(PX_THREADS), (size_t)smem, st, qm, km, P);
+  return launch_pdl(attn_prefix_tc_kernel, dim3((unsigned)(2 * pairs)), dim3(PX_THREADS), (size_t)smem, st, qm, km, P);
 }
 
 }  // namespace csa

@@ -295,6 +295,24 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m; }"
       ::"r"(smem_addr(bar)) : "memory");
 }
+// One lane of a converged warp (the same at every call).  MMA loops are walked by the whole warp and issue inside
+// `if (elect_one())`: loop variables and descriptors then stay in the uniform registers that the instruction reads.
+// Measured for 16-deep MMAs at run-time addresses: 58 cycles each so, 73 in a loop of one lane, 75 predicated.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
+  return r != 0;
+}
+__device__ __forceinline__ void mma_bf16_ss_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile("{ .reg .pred p; setp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p; }"
+               ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc) : "memory");
+}
+// Arrive on an mbarrier of any CTA of the cluster (shared::cluster address).  The release is the CTA's: what the pair's
+// MMAs read was written to the arriving CTA's own shared memory and made visible to the async proxy by
+// fence_proxy_async_smem() before; a cluster-wide release would wait for every access in flight.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
 // Arrivals that say "this warp has read its tensor memory" (after tcgen05.wait::ld and the fence before a thread
 // sync) and publish no ordinary memory: relaxed, as a release waits for every load in flight, prefetched scales
 // included (measured at several hundred cycles an arrival).  The second form takes a shared::cluster address.
