@@ -583,10 +583,12 @@ void attn_tc_plan(const csa_attn_args* a, int hca, int first, int* splits, int* 
 bool attn_tc_cluster(int splits);
 csa_status launch_attn_tc(const csa_attn_args* a, int hca, int first, int splits, int slots, int tpc, uint16_t* part_o,
                           float* part_lse, cudaStream_t st);
-// attention over a shared prefix (attn_prefix_tc.cu)
-void attn_prefix_plan(long long R, int n_p, int most, int* pairs, int* slots);
-csa_status launch_attn_prefix(const csa_attn_args* a, const void* prefix, int n_p, int pairs, int slot0, int pslots, int slots,
-                              uint16_t* part_o, float* part_lse, cudaStream_t st);
+// attention over a shared prefix (attn_prefix_tc.cu), the own keys as rows for it (unpack.cu)
+bool attn_prefix_takes_own(const csa_attn_args* a, int n_p);
+void attn_prefix_plan(const csa_attn_args* a, int n_p, bool own, int most, int* pairs, int* slots);
+csa_status launch_attn_prefix(const csa_attn_args* a, const void* prefix, int n_p, const void* own_rows, int pairs, int slot0,
+                              int pslots, int slots, uint16_t* part_o, float* part_lse, cudaStream_t st);
+csa_status launch_own_rows(const csa_attn_args* a, int first, void* out, cudaStream_t st);
 
 bool attn_tc_eligible(const csa_attn_args* a, int hca, int max_splits);
 
@@ -723,22 +725,102 @@ static csa_status run_attn(const csa_attn_args* a, void* ws, size_t ws_bytes, vo
                              a->out_rope_theta, st);
 }
 
-// ---- HCA with a shared prefix: the sequences' own keys (entries from n_p on, and the window) by the attention above
-// and the prefix by attn_prefix_tc_kernel, each leaving partials in the query's slots [own | prefix]; one merge.
+// Merge of many partials of few rows: one CTA a row, its 8 warps take the slots in turn (the merge above walks them six
+// at a time with one warp: 34 slots of 64 rows took it 16 us).
+constexpr int MERGE_WIDE_WARPS = 8, MERGE_WIDE_FROM = 7;
+
+__global__ void __launch_bounds__(MERGE_WIDE_WARPS * 32)
+    attn_merge_wide_kernel(const uint16_t* __restrict__ part_o, const float* __restrict__ part_lse, int slots, int H,
+                           uint16_t* __restrict__ out, float* __restrict__ lse, const int64_t* __restrict__ q_pos,
+                           float rope_theta) {
+  __shared__ float4 sum_o[MERGE_WIDE_WARPS][4][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long bq = blockIdx.x / H;
+  const int h = (int)(blockIdx.x % H);
+  pdl_trigger();
+  pdl_wait();
+  const uint16_t* base = part_o + (bq * slots * H + h) * 512LL + lane * 16;
+  const float* lrow = part_lse + bq * slots * H + h;
+  float mx = -INFINITY, sum = 0.f;
+  for (int s = lane; s < slots; s += 32) mx = fmaxf(mx, lrow[(long long)s * H]);
+  mx = warp_max(mx);
+  for (int s = lane; s < slots; s += 32) {
+    const float v = lrow[(long long)s * H];
+    sum += v == -INFINITY ? 0.f : exp2f((v - mx) * LOG2E);
+  }
+  sum = warp_sum(sum);
+  float acc[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+  for (int s0 = warp; s0 < slots; s0 += 4 * MERGE_WIDE_WARPS) {
+    PartDims<uint16_t, 16> v[4];
+    float w[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int s = s0 + c * MERGE_WIDE_WARPS;
+      const float ls = s < slots ? lrow[(long long)s * H] : -INFINITY;
+      w[c] = ls == -INFINITY ? 0.f : exp2f((ls - mx) * LOG2E);      // (a slot without keys was not written)
+      if (w[c] != 0.f) v[c].load(base + (long long)s * H * 512);
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (w[c] != 0.f)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[i] = fmaf(w[c], v[c].get(i), acc[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) sum_o[warp][i][lane] = make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+  __syncthreads();
+  if (warp != 0) return;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float4 t = sum_o[0][i][lane];
+#pragma unroll
+    for (int r = 1; r < MERGE_WIDE_WARPS; ++r) {
+      const float4 u = sum_o[r][i][lane];
+      t.x += u.x; t.y += u.y; t.z += u.z; t.w += u.w;
+    }
+    acc[4 * i] = t.x * inv; acc[4 * i + 1] = t.y * inv; acc[4 * i + 2] = t.z * inv; acc[4 * i + 3] = t.w * inv;
+  }
+  if (rope_theta != 0.f) inverse_rope_lanes<512>(acc, lane, q_pos[bq], rope_theta);
+  uint32_t pk[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) pk[i] = pack_bf16x2(acc[2 * i], acc[2 * i + 1]);
+  uint4* o = reinterpret_cast<uint4*>(out + (bq * H + h) * 512LL + lane * 16);
+  o[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+  o[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+  if (lse && lane == 0) lse[bq * H + h] = sum == 0.f ? -INFINITY : mx + logf(sum);
+}
+
+static csa_status launch_merge_wide(const uint16_t* po, const float* pl, int slots, int H, long long rows, uint16_t* out,
+                                    float* lse, const int64_t* q_pos, float rope_theta, cudaStream_t st) {
+  static std::atomic<unsigned> attr_done{0};
+  set_smem_once((const void*)attn_merge_wide_kernel, 0, attr_done);
+  return launch_pdl(attn_merge_wide_kernel, dim3((unsigned)(rows * H)), dim3(MERGE_WIDE_WARPS * 32), 0, st, po, pl, slots, H,
+                    out, lse, q_pos, rope_theta);
+}
+
+// ---- HCA with a shared prefix: the prefix by attn_prefix_tc_kernel, the sequences' own keys (entries from n_p on, and
+// the window) by the same kernel or by the attention above, each leaving partials in the query's slots; one merge.
 struct SharedPlan {
-  int own, tpc;           // splits of the own keys (0: there are none), their tiles per CTA
+  int own, tpc;           // splits of the own keys in the per-query attention (0: not there), their tiles per CTA
+  bool rows;              // own keys in the prefix kernel
   int pairs, pslots;      // the prefix kernel's
-  size_t off_lse, total;
+  size_t off_lse, off_rows, total;
 };
 
 static SharedPlan plan_shared(const csa_shared_attn_args* s) {
   const csa_attn_args* a = &s->attn;
   SharedPlan p{};
-  if (a->n_max > s->n_prefix || attn_has_window(a)) attn_tc_plan(a, 1, s->n_prefix, &p.own, &p.tpc);
-  attn_prefix_plan((long long)a->B * a->Nq * a->H, s->n_prefix, MERGE_MAX_SPLITS, &p.pairs, &p.pslots);
+  const long long own = (long long)a->n_max - s->n_prefix + (attn_has_window(a) ? a->Wn : 0);
+  p.rows = own > 0 && attn_prefix_takes_own(a, s->n_prefix);
+  if (own > 0 && !p.rows) attn_tc_plan(a, 1, s->n_prefix, &p.own, &p.tpc);
+  attn_prefix_plan(a, s->n_prefix, p.rows, MERGE_MAX_SPLITS, &p.pairs, &p.pslots);
   const size_t parts = (size_t)a->B * a->Nq * (p.own + p.pslots) * a->H;
   p.off_lse = align_up(parts * 512 * 2, 256);
-  p.total = align_up(p.off_lse + parts * 4, 256);
+  p.off_rows = align_up(p.off_lse + parts * 4, 256);
+  p.total = p.off_rows + (p.rows ? (size_t)a->B * own * 1024 : 0);
   return p;
 }
 
@@ -770,10 +852,15 @@ static csa_status run_shared(const csa_shared_attn_args* s, void* ws, size_t ws_
   uint16_t* po = (uint16_t*)ws;
   float* pl = (float*)((uint8_t*)ws + p.off_lse);
   const int slots = p.own + p.pslots;
+  void* own_rows = p.rows ? (uint8_t*)ws + p.off_rows : nullptr;
   csa_status r = CSA_OK;
+  if (p.rows) r = launch_own_rows(a, s->n_prefix, own_rows, st);
   if (p.own > 0) r = launch_attn_tc(a, 1, s->n_prefix, p.own, slots, p.tpc, po, pl, st);
-  if (r == CSA_OK) r = launch_attn_prefix(a, s->prefix_kv, s->n_prefix, p.pairs, p.own, p.pslots, slots, po, pl, st);
+  if (r == CSA_OK)
+    r = launch_attn_prefix(a, s->prefix_kv, s->n_prefix, own_rows, p.pairs, p.own, p.pslots, slots, po, pl, st);
   if (r != CSA_OK) return r;
+  if (slots >= MERGE_WIDE_FROM)
+    return launch_merge_wide(po, pl, slots, a->H, rows, (uint16_t*)a->out, a->lse, a->q_pos, a->out_rope_theta, st);
   return launch_merge<uint16_t>(po, pl, slots, a->H, a->d, rows, (uint16_t*)a->out, a->lse, a->q_pos, a->out_rope_theta, st);
 }
 

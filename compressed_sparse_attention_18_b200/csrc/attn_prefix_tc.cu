@@ -22,6 +22,8 @@
 //   O  (1)    new  new  kept kept new  new  kept kept     dims 128 c + 64 (j & 1) .. in 0-3, 256 more in 4-7)
 // Softmax: a row's reference m moves only when a tile's scores exceed it by more than 2^8 (or in a part's first tile),
 // which the CTA's threads agree on with one barrier; a thread sums its own columns until the part ends.
+// A block's last tiles can be the own keys of the sequences it touches (bf16 rows from own_rows_kernel), masked to the rows
+// of their sequence and to what each sees.
 // Parts: the tiles of all blocks of 128 rows form one line that is cut evenly over the pairs, so a pair works on the end
 // of one block and the start of the next, and each leaves a partial (O / l in bf16, lse) that the split merge adds.
 // Every wait is bounded; a wait that gives up records device error 1 and the kernel leaves.
@@ -60,8 +62,12 @@ struct PxSmem {
 struct PxParams {
   long long R;            // query rows: B * Nq * H
   long long T;            // tiles of all blocks
-  int tiles;              // tiles of one block: ceil(n_p / 256)
-  int Nq, H, ratio, n_p, n_max;
+  int tiles;              // tiles of one block: of the prefix, then nseq * otiles of own keys
+  int ptiles;             // tiles of the prefix: ceil(n_p / 256)
+  int nseq, otiles;       // own keys: sequences a block can touch, tiles of one sequence (0: attended elsewhere)
+  int B, Nq, H, ratio, n_p, n_max;
+  int E, Wn, window;      // own rows of a sequence: entries n_p .. n_p + E - 1, then Wn window rows
+  const int64_t* win_pos0;
   int slot0, slots;       // partial slots of a query: this kernel's first, and all
   int pslots;             // this kernel's
   float scale_log2;
@@ -73,6 +79,25 @@ struct PxParams {
 
 // The pair that tile g of the line belongs to when it is cut into G even parts [i T / G, (i + 1) T / G).
 __host__ __device__ __forceinline__ long long px_pair_of(long long g, long long G, long long T) { return ((g + 1) * G - 1) / T; }
+
+// Tile i of a block: prefix rows from row0 on (b = -1), or own rows of sequence b, its keys key0 on.
+struct PxTile {
+  int b, key0, row0;
+};
+__device__ __forceinline__ PxTile px_tile(const PxParams& P, long long blk, int i) {
+  PxTile t;
+  if (i < P.ptiles) {
+    t.b = -1;
+    t.key0 = t.row0 = i * PX_KEYS;
+  } else {
+    const int o = i - P.ptiles, s = o / P.otiles;
+    t.b = (int)(blk * PX_ROWS / ((long long)P.Nq * P.H)) + s;
+    t.key0 = (o - s * P.otiles) * PX_KEYS;
+    // (a sequence behind the last: some rows that no query row is matched with)
+    t.row0 = min(t.b, P.B - 1) * (P.E + P.Wn) + t.key0;
+  }
+  return t;
+}
 
 __device__ __forceinline__ float px_exp2(float x) {
   float y;
@@ -91,7 +116,7 @@ __device__ __forceinline__ bool px_any(bool v) {
 
 __global__ void __launch_bounds__(PX_THREADS, 1) __cluster_dims__(2, 1, 1)
     attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
-                          const PxParams P) {
+                          const __grid_constant__ CUtensorMap omap, const PxParams P) {
   extern __shared__ uint8_t smem_raw[];
   PxSmem& S = *reinterpret_cast<PxSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -109,6 +134,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) __cluster_dims__(2, 1, 1)
     fence_mbar_init();
     prefetch_tensormap(&qmap);
     prefetch_tensormap(&kmap);
+    if (P.otiles > 0) prefetch_tensormap(&omap);
   }
   if (warp == 9) { tmem_alloc_pair(&S.tmem_base, 512); tmem_relinquish_pair(); }
   pdl_trigger();
@@ -131,18 +157,19 @@ __global__ void __launch_bounds__(PX_THREADS, 1) __cluster_dims__(2, 1, 1)
         for (int j = 0; j < 8; ++j)
           tma_load_2d_pair(S.Q[j], &qmap, j * 64, (int)(blk * PX_ROWS) + 64 * rank, peer_addr(&S.bar_q, 0));
         for (; g < e && ok; ++g, ++tile) {
-          const int key0 = (int)(g - blk * P.tiles) * PX_KEYS;
+          const PxTile w = px_tile(P, blk, (int)(g - blk * P.tiles));
+          const CUtensorMap* map = w.b < 0 ? &kmap : &omap;
           for (int j = 0; j < 8 && ok; ++j) {
             if (tile > 0 && !mbar_wait(&S.rel[j], 1)) { ok = false; break; }      // read by the previous tile's O
             if (rank == 0) mbar_arrive_expect_tx(&S.full[j], 2 * PX_CHUNK);
-            tma_load_2d_pair(S.K[j], &kmap, j * 64, key0 + 128 * rank, peer_addr(&S.full[j], 0));
+            tma_load_2d_pair(S.K[j], map, j * 64, w.row0 + 128 * rank, peer_addr(&S.full[j], 0));
           }
           for (int j = 0; j < 8 && ok; ++j) {
             if (!mbar_wait(&S.rel[j], 0)) { ok = false; break; }                  // read by S
             const int owner = (j & 2) ? 0 : 1;                                    // whose chunk is not the one O wants
             if (rank == 0) mbar_arrive_expect_tx(&S.full[j], PX_CHUNK);
             if (rank == owner)
-              tma_load_2d_pair(S.K[j], &kmap, ((j & 4) ? 256 : 0) + 128 * rank + 64 * (j & 1), key0 + ((j & 2) ? 128 : 0),
+              tma_load_2d_pair(S.K[j], map, ((j & 4) ? 256 : 0) + 128 * rank + 64 * (j & 1), w.row0 + ((j & 2) ? 128 : 0),
                                peer_addr(&S.full[j], 0));
           }
         }
@@ -231,37 +258,48 @@ __global__ void __launch_bounds__(PX_THREADS, 1) __cluster_dims__(2, 1, 1)
       // stored), and its place in the partials without the slot
       const long long qr = blk * PX_ROWS + 64 * rank + row;
       const bool real = qr < P.R;
-      int nv = P.n_p;
+      // (own keys 0 .. ve - 1 are visible entries, wl .. wh - 1 the window)
+      int nv = P.n_p, b = -2, ve = 0, wl = 0, wh = 0;
       long long prt = 0;
       if (real) {
-        const long long bq = qr / P.H;
-        const int b = (int)(bq / P.Nq);
-        const long long see = (P.q_pos[bq] + 1) / P.ratio;
-        nv = (int)max(0LL, min((long long)min(P.n_p, min(P.n_c[b], P.n_max)), see));
+        const long long bq = qr / P.H, tq = P.q_pos[bq];
+        b = (int)(bq / P.Nq);
+        const int see = (int)max(0LL, min((long long)min(P.n_c[b], P.n_max), (tq + 1) / P.ratio));
+        nv = min(P.n_p, see);
+        ve = max(0, see - P.n_p);
+        if (P.otiles > 0 && P.Wn > 0) {
+          const long long p0 = P.win_pos0[b], lo = max(max(0LL, tq - P.window + 1), p0), hi = min(tq, p0 + P.Wn - 1);
+          if (hi >= lo) { wl = P.E + (int)(lo - p0); wh = P.E + (int)(hi - p0) + 1; }
+        }
         prt = bq * P.slots * P.H + (qr - bq * P.H);
       }
       float m = -INFINITY;                       // the row's reference (log2 units); its four threads agree
       float l = 0.f;                             // this thread's part of the row's sum
       for (long long t = g; t < e; ++t, ++f) {
         const bool first = t == g;
-        // keys of this thread that the row sees
-        const int lim = nv - ((int)(t - blk * P.tiles) * PX_KEYS + 64 * kq);
+        const PxTile w = px_tile(P, blk, (int)(t - blk * P.tiles));
+        const int k0 = w.key0 + 64 * kq;         // this thread's first key
         ok = ok && mbar_wait(&S.bar_s, f & 1);
         tc_fence_after();
         float z[64];
         {
-          uint32_t v[32], w[32];
+          uint32_t v[32], u[32];
           tmem_ld_x32(lane_base + PX_COL_S + 64 * ch, v);
-          tmem_ld_x32(lane_base + PX_COL_S + 64 * ch + 32, w);
+          tmem_ld_x32(lane_base + PX_COL_S + 64 * ch + 32, u);
           tmem_wait_ld_x32(v);
-          tmem_wait_ld_x32(w);
+          tmem_wait_ld_x32(u);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) { z[j] = __uint_as_float(v[j]); z[j + 32] = __uint_as_float(w[j]); }
+          for (int j = 0; j < 32; ++j) { z[j] = __uint_as_float(v[j]); z[j + 32] = __uint_as_float(u[j]); }
         }
-        if (lim < 64) {
+        if (w.b >= 0) {
+          const int e0 = w.b == b ? ve - k0 : 0, w0 = wl - k0, w1 = w.b == b ? wh - k0 : w0;
 #pragma unroll
           for (int j = 0; j < 64; ++j)
-            if (j >= lim) z[j] = -INFINITY;
+            if (!(j < e0 || (j >= w0 && j < w1))) z[j] = -INFINITY;
+        } else if (k0 + 64 > nv) {
+#pragma unroll
+          for (int j = 0; j < 64; ++j)
+            if (k0 + j >= nv) z[j] = -INFINITY;
         }
         float top = z[0];
 #pragma unroll
@@ -360,10 +398,37 @@ __global__ void __launch_bounds__(PX_THREADS, 1) __cluster_dims__(2, 1, 1)
   }
 }
 
-// The prefix kernel's plan for R query rows over n_p entries: pairs of CTAs, and partial slots a query needs (at most
-// `most`).
-void attn_prefix_plan(long long R, int n_p, int most, int* pairs, int* slots) {
-  const long long blocks = (R + PX_ROWS - 1) / PX_ROWS, tiles = ((long long)n_p + PX_KEYS - 1) / PX_KEYS, T = blocks * tiles;
+// Tiles of own keys that a block of rows has when the prefix kernel takes them too: the sequences it can touch, and the
+// tiles of one.
+static void px_own(const csa_attn_args* a, int n_p, int* nseq, int* otiles) {
+  const long long rs = (long long)a->Nq * a->H;             // rows of a sequence
+  const long long n = PX_ROWS % rs == 0 ? PX_ROWS / rs : rs % PX_ROWS == 0 ? 1 : (PX_ROWS + rs - 2) / rs + 1;
+  *nseq = (int)(n < a->B ? n : a->B);
+  *otiles = (int)(((long long)a->n_max - n_p + (attn_has_window(a) ? a->Wn : 0) + PX_KEYS - 1) / PX_KEYS);
+}
+
+// Whether the prefix kernel takes the own keys too (as bf16 rows written by own_rows_kernel), or the per-query attention
+// does: by their times.  A tile takes a pair 4.0 us, rows are written at about 4 TB/s; the per-query kernels take about
+// 10 us and 6.9 us a tile of 128 keys on an SM (TA_TILE_US).
+bool attn_prefix_takes_own(const csa_attn_args* a, int n_p) {
+  int nseq, otiles;
+  px_own(a, n_p, &nseq, &otiles);
+  const double rows = (double)a->B * a->Nq, R = rows * a->H;
+  const double own = (double)a->n_max - n_p + (attn_has_window(a) ? a->Wn : 0);
+  if (own * a->B > 2147483647.0) return false;
+  const double blocks = (double)((long long)(R + PX_ROWS - 1) / PX_ROWS);
+  const double t_here = 4.0 * blocks * nseq * otiles / 74 + a->B * own * 1.4e3 / 4e6;
+  const double waves = (double)(long long)((rows * (double)(long long)((own + 127) / 128) + 147) / 148);
+  return t_here < 10.0 + 6.9 * waves;
+}
+
+// The prefix kernel's plan: pairs of CTAs, and partial slots a query needs (at most `most`).
+void attn_prefix_plan(const csa_attn_args* a, int n_p, bool own, int most, int* pairs, int* slots) {
+  const long long R = (long long)a->B * a->Nq * a->H;
+  int nseq = 0, otiles = 0;
+  if (own) px_own(a, n_p, &nseq, &otiles);
+  const long long blocks = (R + PX_ROWS - 1) / PX_ROWS;
+  const long long tiles = ((long long)n_p + PX_KEYS - 1) / PX_KEYS + (long long)nseq * otiles, T = blocks * tiles;
   long long G = T < 74 ? T : 74;
   if (G > blocks * (most - 1)) G = blocks * (most - 1);    // a block is cut into at most ceil(G / blocks) + 1 parts
   long long worst = 1;
@@ -379,10 +444,11 @@ void attn_prefix_plan(long long R, int n_p, int most, int* pairs, int* slots) {
   *slots = (int)worst;
 }
 
-csa_status launch_attn_prefix(const csa_attn_args* a, const void* prefix, int n_p, int pairs, int slot0, int pslots, int slots,
-                              uint16_t* part_o, float* part_lse, cudaStream_t st) {
+// own_rows: own_rows_kernel's output, or null (the own keys are attended elsewhere).
+csa_status launch_attn_prefix(const csa_attn_args* a, const void* prefix, int n_p, const void* own_rows, int pairs, int slot0,
+                              int pslots, int slots, uint16_t* part_o, float* part_lse, cudaStream_t st) {
   const long long R = (long long)a->B * a->Nq * a->H;
-  CUtensorMap qm, km;
+  CUtensorMap qm, km, om;
   auto encode = [](CUtensorMap* map, const void* base, long long rows, int box) {
     const cuuint64_t gdim[2] = {512, (cuuint64_t)rows};
     const cuuint64_t gstride[1] = {1024};
@@ -392,10 +458,19 @@ csa_status launch_attn_prefix(const csa_attn_args* a, const void* prefix, int n_
                                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   };
-  if (!encode(&qm, a->q, R, 64) || !encode(&km, prefix, n_p, 128)) return CSA_ERR_CUDA;
   PxParams P{};
+  P.E = a->n_max - n_p;
+  P.Wn = attn_has_window(a) ? a->Wn : 0;
+  if (!encode(&qm, a->q, R, 64) || !encode(&km, prefix, n_p, 128)) return CSA_ERR_CUDA;
+  if (own_rows == nullptr)
+    om = km;                                   // never read
+  else if (!encode(&om, own_rows, (long long)a->B * (P.E + P.Wn), 128))
+    return CSA_ERR_CUDA;
   P.R = R;
-  P.tiles = (n_p + PX_KEYS - 1) / PX_KEYS;
+  P.ptiles = (n_p + PX_KEYS - 1) / PX_KEYS;
+  if (own_rows) px_own(a, n_p, &P.nseq, &P.otiles);
+  P.tiles = P.ptiles + P.nseq * P.otiles;
+  P.B = a->B; P.window = a->window; P.win_pos0 = a->win_pos0;
   P.T = (R + PX_ROWS - 1) / PX_ROWS * P.tiles;
   P.Nq = a->Nq; P.H = a->H; P.ratio = a->ratio; P.n_p = n_p; P.n_max = a->n_max;
   P.slot0 = slot0; P.slots = slots; P.pslots = pslots;
@@ -405,7 +480,7 @@ csa_status launch_attn_prefix(const csa_attn_args* a, const void* prefix, int n_
   static_assert(sizeof(PxSmem) + 1024 <= 232448, "shared memory of a CTA");
   static std::atomic<unsigned> attr_done{0};
   set_smem_once((const void*)attn_prefix_tc_kernel, smem, attr_done);
-  return launch_pdl(attn_prefix_tc_kernel, dim3((unsigned)(2 * pairs)), dim3(PX_THREADS), (size_t)smem, st, qm, km, P);
+  return launch_pdl(attn_prefix_tc_kernel, dim3((unsigned)(2 * pairs)), dim3(PX_THREADS), (size_t)smem, st, qm, km, om, P);
 }
 
 }  // namespace csa

@@ -26,6 +26,31 @@ struct UnpackParams {
   csa_page_map pm;
 };
 
+// Eight channels as bf16: of an FP4 entry (4 code bytes, scale byte, global scale), of an FP8 row (8 codes, scale).
+__device__ __forceinline__ uint4 fp4x8_to_bf16(uint32_t codes, uint32_t scale, float g) {
+  const float sc = e4m3_to_f32(scale);
+  uint32_t y[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t h2 = e2m1x2_to_h2(codes >> (8 * k));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+    y[k] = pack_bf16x2(__fmul_rn(f.x * sc, g), __fmul_rn(f.y * sc, g));
+  }
+  return make_uint4(y[0], y[1], y[2], y[3]);
+}
+__device__ __forceinline__ uint4 fp8x8_to_bf16(uint32_t c0, uint32_t c1, float sc) {
+  uint32_t y[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint32_t h2;
+    const uint16_t two = (uint16_t)((k < 2 ? c0 : c1) >> (16 * (k & 1)));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(two));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+    y[k] = pack_bf16x2(__fmul_rn(f.x, sc), __fmul_rn(f.y, sc));
+  }
+  return make_uint4(y[0], y[1], y[2], y[3]);
+}
+
 // One warp writes one row, a lane two chunks of 8 channels (16 bytes) at a time, both loaded before either is used; the
 // many small warps keep more reads in flight than several rows a warp (32768 FP4 entries: 11.8 us, 3.9 TB/s; two rows
 // 12.9, four 17.4).
@@ -65,27 +90,89 @@ __global__ void __launch_bounds__(256) unpack_kernel(const UnpackParams P) {
     for (int u = 0; u < 2; ++u) {
       if (c0 + 32 * u >= P.cpr) continue;
       uint4 v = raw[u];
-      if (8 * (c0 + 32 * u) < P.d_n) {
-        uint32_t y[4];
-        const float sc = FP8 ? s[u] : e4m3_to_f32(raw[u].y);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t h2;
-          if (FP8) {
-            const uint16_t two = (uint16_t)((k < 2 ? raw[u].x : raw[u].y) >> (16 * (k & 1)));
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(two));
-          } else {
-            h2 = e2m1x2_to_h2(raw[u].x >> (8 * k));
-          }
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-          y[k] = FP8 ? pack_bf16x2(__fmul_rn(f.x, sc), __fmul_rn(f.y, sc))
-                     : pack_bf16x2(__fmul_rn(f.x * sc, P.g), __fmul_rn(f.y * sc, P.g));
-        }
-        v = make_uint4(y[0], y[1], y[2], y[3]);
-      }
+      if (8 * (c0 + 32 * u) < P.d_n) v = FP8 ? fp8x8_to_bf16(raw[u].x, raw[u].y, s[u]) : fp4x8_to_bf16(raw[u].x, raw[u].y, P.g);
       reinterpret_cast<uint4*>(P.out)[(unsigned long long)r * P.cpr + c0 + 32 * u] = v;
     }
   }
+}
+
+// A sequence's own keys for the shared-prefix attention, bf16 rows of 512: cache entries first .. n_max - 1 (zero from
+// n_c on: the cache holds anything there), then the window buffer.  One warp per row as above.
+struct OwnRowsParams {
+  uint32_t total, per;     // rows, and of one sequence: E entries, then the window's
+  int first, E, n_max, Wn;
+  float g;
+  const int32_t* n_c;
+  const uint8_t* codes;
+  const uint8_t* scales;
+  const uint16_t* rope;
+  const uint16_t* win;     // bf16 window, or null:
+  const uint8_t* wcodes;
+  const float* wscales;
+  const uint16_t* wrope;
+  uint16_t* out;
+  csa_page_map pm;
+};
+
+__global__ void __launch_bounds__(256) own_rows_kernel(const OwnRowsParams P) {
+  const uint32_t r = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  pdl_trigger();
+  pdl_wait();
+  if (r >= P.total) return;
+  const int b = (int)(r / P.per), u = (int)(r % P.per);
+  uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+  if (u < P.E) {
+    const int i = P.first + u;
+    const long long row = i < min(__ldg(P.n_c + b), P.n_max) ? page_row(P.pm, b, P.n_max, i) : -1;
+    if (row >= 0) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int c = lane + 32 * k;
+        if (c >= 56)
+          v[k] = __ldg(reinterpret_cast<const uint4*>(P.rope + row * 64) + (c - 56));
+        else
+          v[k] = fp4x8_to_bf16(__ldg(reinterpret_cast<const uint32_t*>(P.codes + row * 224) + c), __ldg(P.scales + row * 16 + (c >> 2)), P.g);
+      }
+    }
+  } else {
+    const long long row = (long long)b * P.Wn + (u - P.E);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int c = lane + 32 * k;
+      if (P.win) {
+        v[k] = __ldg(reinterpret_cast<const uint4*>(P.win + row * 512) + c);
+      } else if (c >= 56) {
+        v[k] = __ldg(reinterpret_cast<const uint4*>(P.wrope + row * 64) + (c - 56));
+      } else {
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(P.wcodes + row * 448) + c);
+        v[k] = fp8x8_to_bf16(w.x, w.y, __ldg(P.wscales + row * 8 + (c >> 3)));
+      }
+    }
+  }
+  uint4* o = reinterpret_cast<uint4*>(P.out + (size_t)r * 512);
+  o[lane] = v[0];
+  o[lane + 32] = v[1];
+}
+
+// Writes [B][n_max - first + Wn][512]; the caller checked shapes and alignment (d = 512, d_rope = 64).
+csa_status launch_own_rows(const csa_attn_args* a, int first, void* out, cudaStream_t st) {
+  OwnRowsParams P{};
+  const bool has_win = attn_has_window(a);
+  P.first = first; P.E = a->n_max - first; P.n_max = a->n_max; P.Wn = has_win ? a->Wn : 0;
+  const long long per = (long long)P.E + P.Wn, total = per * a->B;
+  CSA_SUPPORTED(total <= 0x7fffffffLL);
+  P.per = (uint32_t)per; P.total = (uint32_t)total;
+  P.g = a->g_kv; P.n_c = a->n_c; P.codes = a->kv_codes; P.scales = a->kv_scales; P.rope = (const uint16_t*)a->kv_rope;
+  if (a->win_format == CSA_WIN_FP8) {
+    P.wcodes = a->win_codes; P.wscales = a->win_scales; P.wrope = (const uint16_t*)a->win_rope;
+  } else {
+    P.win = (const uint16_t*)a->win_kv;
+  }
+  P.out = (uint16_t*)out; P.pm = a->kv_pages;
+  static std::atomic<unsigned> attr_done{0};
+  set_smem_once((const void*)own_rows_kernel, 0, attr_done);
+  return launch_pdl(own_rows_kernel, dim3((unsigned)((total + 7) / 8)), dim3(256), 0, st, P);
 }
 
 template <bool FP8>

@@ -43,7 +43,7 @@ class Case:
         self.cache.rope.fill_(float("nan"))
         if own:
             csa.pack_fp4(rows, self.cache, row0=torch.full((B,), n_p, dtype=torch.int32, device=DEV))
-        self.own = [O.entry_kv(*O.pack_fp4(f64(rows[b]), DR, 1.0), D - DR, 1.0) if own else np.zeros((0, D)) for b in range(B)]
+        self.own = lambda b: O.entry_kv(*O.pack_fp4(f64(rows[b]), DR, 1.0), D - DR, 1.0) if own else np.zeros((0, D))
         self.win = self.win_pos0 = None
         self.win_rows = np.zeros((B, 0, D))
         p0 = self.t[:, 0] - W + 1
@@ -68,7 +68,7 @@ class Case:
     def check(self, out, lse, scale=D ** -0.5, theta=0.0, rows=None, atol=OUT_ATOL, rtol=OUT_RTOL):
         pre = f64(self.prefix)
         for b in (range(len(self.n_c)) if rows is None else rows):
-            kv = np.concatenate([pre, self.own[b]])
+            kv = np.concatenate([pre, self.own(b)])
             ro, rl = O.hca_attention(f64(self.q[b]), self.t[b], kv, int(self.n_c[b]), self.r, self.win_rows[b], int(self.p0[b]), W,
                                      scale, out_rope_theta=theta, d_rope=DR)
             assert_close(f64(out[b]), ro, atol, rtol, f"out b={b}")
@@ -146,6 +146,16 @@ def test_same_as_the_unshared_attention(cuda_lib):
     assert_close(f64(lse), f64(rl), LSE_ATOL, LSE_RTOL)
     c.prefix = args[4]
     c.check(out, lse, rows=(0, 41, 95))
+
+
+@pytest.mark.parametrize("B,Nq,H,n_p,own,fp8", [(40, 1, 16, 200, 3000, False), (40, 1, 16, 200, 3000, True),
+                                                (3, 1, 64, 300, 600, False), (130, 1, 1, 300, 9, False), (9, 3, 7, 300, 50, True)])
+def test_own_keys_long_and_many(cuda_lib, B, Nq, H, n_p, own, fp8):
+    """Own entries that outnumber the prefix in many sequences (attended query by query), several tiles of them in few
+    sequences, and blocks of rows that touch many sequences or cut them at odd places."""
+    c = Case(cuda_lib, B, Nq, H, n_p, own, fp8=fp8, seed=B)
+    out, lse = c.run(cuda_lib)
+    c.check(out, lse, rows=(0, B // 2, B - 1))
 
 
 def test_no_prefix_is_the_plain_attention(cuda_lib):
