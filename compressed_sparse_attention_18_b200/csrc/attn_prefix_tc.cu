@@ -52,7 +52,7 @@ struct PxSmem {
   float red[4][64];                         // [key quarter][row]
   alignas(8) uint64_t full[8];              // rank 0: a slot's operands have landed in both CTAs (twice a tile: S, O)
   uint64_t rel[8];                          // both: a slot has been read (twice a tile: by S, by O)
-  uint64_t bar_q;                           // rank 0: Q has landed in both
+  uint64_t bar_q[8];                        // rank 0: a dim block of Q has landed in both
   uint64_t bar_qfree, bar_s, bar_o;         // both: Q read; S complete; O complete
   uint64_t bar_p;                           // rank 0: P written (and S read) in both
   uint32_t tmem_base;
@@ -125,8 +125,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) __cluster_dims__(2, 1, 1)
   const long long g_begin = pair * P.T / G, g_end = (pair + 1) * P.T / G;
   if (tid == 0) {
     S.err = 0;
-    for (int i = 0; i < 8; ++i) { mbar_init(&S.full[i], 1); mbar_init(&S.rel[i], 1); }
-    mbar_init(&S.bar_q, 1);
+    for (int i = 0; i < 8; ++i) { mbar_init(&S.full[i], 1); mbar_init(&S.rel[i], 1); mbar_init(&S.bar_q[i], 1); }
     mbar_init(&S.bar_qfree, 1);
     mbar_init(&S.bar_s, 1);
     mbar_init(&S.bar_o, 1);
@@ -153,17 +152,20 @@ __global__ void __launch_bounds__(PX_THREADS, 1) __cluster_dims__(2, 1, 1)
         const long long blk = g / P.tiles, blk_end = (blk + 1) * P.tiles, e = blk_end < g_end ? blk_end : g_end;
         // the previous part's S MMAs have read Q
         if (part > 0 && !mbar_wait(&S.bar_qfree, (part - 1) & 1)) { ok = false; break; }
-        if (rank == 0) mbar_arrive_expect_tx(&S.bar_q, 2 * 8 * 64 * 128);
-        for (int j = 0; j < 8; ++j)
-          tma_load_2d_pair(S.Q[j], &qmap, j * 64, (int)(blk * PX_ROWS) + 64 * rank, peer_addr(&S.bar_q, 0));
+        bool q_due = true;                       // Q's dim blocks go with the first tile's chunks
         for (; g < e && ok; ++g, ++tile) {
           const PxTile w = px_tile(P, blk, (int)(g - blk * P.tiles));
           const CUtensorMap* map = w.b < 0 ? &kmap : &omap;
           for (int j = 0; j < 8 && ok; ++j) {
             if (tile > 0 && !mbar_wait(&S.rel[j], 1)) { ok = false; break; }      // read by the previous tile's O
+            if (q_due) {
+              if (rank == 0) mbar_arrive_expect_tx(&S.bar_q[j], 2 * 64 * 128);
+              tma_load_2d_pair(S.Q[j], &qmap, j * 64, (int)(blk * PX_ROWS) + 64 * rank, peer_addr(&S.bar_q[j], 0));
+            }
             if (rank == 0) mbar_arrive_expect_tx(&S.full[j], 2 * PX_CHUNK);
             tma_load_2d_pair(S.K[j], map, j * 64, w.row0 + 128 * rank, peer_addr(&S.full[j], 0));
           }
+          q_due = false;
           for (int j = 0; j < 8 && ok; ++j) {
             if (!mbar_wait(&S.rel[j], 0)) { ok = false; break; }                  // read by S
             const int owner = (j & 2) ? 0 : 1;                                    // whose chunk is not the one O wants
@@ -195,19 +197,19 @@ __global__ void __launch_bounds__(PX_THREADS, 1) __cluster_dims__(2, 1, 1)
       uint32_t f = 0, part = 0;
       for (long long g = g_begin; g < g_end && ok; ++part) {
         const long long blk_end = (g / P.tiles + 1) * P.tiles, e = blk_end < g_end ? blk_end : g_end;
-        ok = mbar_wait(&S.bar_q, part & 1);
         const int n = (int)(e - g);
 #pragma unroll 1
         for (int t = 0; t < n && ok; ++t, ++f) {
-#pragma unroll
+          // (the loops are kept short: a part's first pass fetches this code from L2)
+#pragma unroll 1
           for (int j = 0; j < 8; ++j) {
+            if (t == 0) landed(&S.bar_q[j], part & 1);
             landed(&S.full[j], 0);
             tc_fence_after();
+            const uint64_t qd = qdesc + (uint64_t)(j * (64 * 128 >> 4)), kd = kdesc + (uint64_t)(j * (PX_CHUNK >> 4));
             if (elect_one()) {
 #pragma unroll
-              for (int s = 0; s < 4; ++s)
-                mma_bf16_ss_pair(tb + PX_COL_S, qdesc + (uint64_t)((j * 64 * 128 + s * 32) >> 4),
-                                 kdesc + (uint64_t)((j * PX_CHUNK + s * 32) >> 4), ids, (j | s) != 0);
+              for (int s = 0; s < 4; ++s) mma_bf16_ss_pair(tb + PX_COL_S, qd + 2 * s, kd + 2 * s, ids, (j | s) != 0);
               mma_commit_pair(&S.rel[j]);
               if (j == 7) {
                 mma_commit_pair(&S.bar_s);
@@ -219,17 +221,18 @@ __global__ void __launch_bounds__(PX_THREADS, 1) __cluster_dims__(2, 1, 1)
           ok = ok && mbar_wait(&S.bar_p, f & 1);
           tc_fence_after();
           // slots 2 i, 2 i + 1: keys 128 (i & 1) .., dims 256 (i >> 1) ..
-#pragma unroll
+#pragma unroll 1
           for (int i = 0; i < 4; ++i) {
             landed(&S.full[2 * i], 1);
             landed(&S.full[2 * i + 1], 1);
             tc_fence_after();
+            const uint64_t pd = pdesc + (uint64_t)((i & 1) * (2 * 64 * 128 >> 4)), vd = vdesc + (uint64_t)(i * (2 * PX_CHUNK >> 4));
+            const uint32_t d = tb + PX_COL_O + 128 * (i >> 1);
             if (elect_one()) {
 #pragma unroll
               for (int s = 0; s < 8; ++s)
-                mma_bf16_ss_pair(tb + PX_COL_O + 128 * (i >> 1),
-                                 pdesc + (uint64_t)(((2 * (i & 1) + (s >> 2)) * 64 * 128 + (s & 3) * 32) >> 4),
-                                 vdesc + (uint64_t)((2 * i * PX_CHUNK + s * 2048) >> 4), ido, t > 0 || (i & 1) || s > 0);
+                mma_bf16_ss_pair(d, pd + (uint64_t)(((s >> 2) * 64 * 128 + (s & 3) * 32) >> 4), vd + 128 * s, ido,
+                                 t > 0 || (i & 1) || s > 0);
               mma_commit_pair(&S.rel[2 * i]);
               mma_commit_pair(&S.rel[2 * i + 1]);
               if (i == 3 && t + 1 == n) mma_commit_pair(&S.bar_o);
@@ -365,22 +368,36 @@ __global__ void __launch_bounds__(PX_THREADS, 1) __cluster_dims__(2, 1, 1)
       }
       ok = ok && mbar_wait(&S.bar_o, part & 1);
       tc_fence_after();
-      // columns 128 ch ..: dims 256 ch + 128 (quad >> 1) ..
-      uint16_t* dst = P.part_o + out * 512 + 256 * ch + 128 * (quad >> 1);
+      // columns 128 ch ..: dims 256 ch + 128 (quad >> 1) .., 64 at a time through this warp's 4 KB of the P buffer (the
+      // O MMAs have read it) so that 8 lanes store 128 bytes of a row (16 bytes a row and store took 6000 cycles)
+      uint8_t* stage = S.P[0] + 4096 * warp;
+      uint16_t* dst = P.part_o + 256 * ch + 128 * (quad >> 1) + 8 * (lane & 7);
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        uint32_t o[32];
-        tmem_ld_x32(lane_base + PX_COL_O + 128 * ch + 32 * c, o);
-        tmem_wait_ld_x32(o);
-        if (real)
+      for (int c = 0; c < 2; ++c) {
+        uint32_t o[2][32];
+        tmem_ld_x32(lane_base + PX_COL_O + 128 * ch + 64 * c, o[0]);
+        tmem_ld_x32(lane_base + PX_COL_O + 128 * ch + 64 * c + 32, o[1]);
+        tmem_wait_ld_x32(o[0]);
+        tmem_wait_ld_x32(o[1]);
+        __syncwarp();                            // the rows of the round before have been read
 #pragma unroll
-          for (int j = 0; j < 32; j += 8) {
-            uint32_t w[4];
+        for (int k = 0; k < 8; ++k) {
+          uint32_t w[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              w[i] = pack_bf16x2(__uint_as_float(o[j + 2 * i]) * inv, __uint_as_float(o[j + 2 * i + 1]) * inv);
-            *reinterpret_cast<uint4*>(dst + 32 * c + j) = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int i = 0; i < 4; ++i) {
+            const int j = 8 * k + 2 * i;
+            w[i] = pack_bf16x2(__uint_as_float(o[j >> 5][j & 31]) * inv, __uint_as_float(o[j >> 5][(j & 31) + 1]) * inv);
           }
+          *reinterpret_cast<uint4*>(stage + lane * 128 + ((k ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int r = 4 * k + (lane >> 3);
+          const long long ro = __shfl_sync(0xffffffffu, real ? out : -1LL, r);
+          const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+          if (ro >= 0) *reinterpret_cast<uint4*>(dst + ro * 512 + 64 * c) = w;
+        }
       }
       tc_fence_before();
       g = e;
