@@ -20,8 +20,9 @@
 //   S  (c)    dims 64 j .. of keys 128 c ..
 //   O  (0)    kept kept new  new  kept kept new  new     (keys 0 .. in slots 0 1 4 5, keys 128 .. in 2 3 6 7;
 //   O  (1)    new  new  kept kept new  new  kept kept     dims 128 c + 64 (j & 1) .. in 0-3, 256 more in 4-7)
-// Softmax: a row's reference m moves only when a tile's scores exceed it by more than 2^8 (or in a part's first tile),
-// which the CTA's threads agree on with one barrier; a thread sums its own columns until the part ends.
+// Softmax: a row's reference m moves only when a tile's scores exceed it by more than 2^8 (or in a part's first tile);
+// the probabilities are written with the old one and the CTA's threads agree afterwards, with one barrier, whether that
+// did; a thread sums its own columns until the part ends.
 // A block's last tiles can be the own keys of the sequences it touches (bf16 rows from own_rows_kernel), masked to the rows
 // of their sequence and to what each sees.
 // Parts: the tiles of all blocks of 128 rows form one line that is cut evenly over the pairs, so a pair works on the end
@@ -38,8 +39,8 @@ using namespace sm100;
 
 constexpr int PX_ROWS = 128;                // query rows of a block: 64 a CTA
 constexpr int PX_KEYS = 256;                // entries of a tile
-constexpr int PX_WORKERS = 256;             // warps 0-7: 4 lane quadrants x 2 halves of a lane's columns
-constexpr int PX_THREADS = PX_WORKERS + 64; // warp 8: TMA, warp 9: tensor memory, MMA (rank 0)
+constexpr int PX_WORKERS = 512;             // warps 0-15: 4 lane quadrants x 4 quarters of a lane's columns
+constexpr int PX_THREADS = PX_WORKERS + 64; // warp 16: TMA, warp 17: tensor memory, MMA (rank 0)
 constexpr int PX_CHUNK = 128 * 128;         // 128 keys x 64 dims bf16
 constexpr uint32_t PX_COL_S = 0, PX_COL_O = 128;
 constexpr float PX_SLACK = 8.0f;            // log2 units: probabilities stay <= 2^8
@@ -49,7 +50,6 @@ struct PxSmem {
   alignas(1024) uint8_t Q[8][64 * 128];     // [dim block][row][128 B], 128-byte swizzle
   alignas(1024) uint8_t K[8][PX_CHUNK];     // [slot][key][128 B], 128-byte swizzle
   alignas(1024) uint8_t P[4][64 * 128];     // [64 keys][row][128 B], 128-byte swizzle
-  float red[4][64];                         // [key quarter][row]
   alignas(8) uint64_t full[8];              // rank 0: a slot's operands have landed in both CTAs (twice a tile: S, O)
   uint64_t rel[8];                          // both: a slot has been read (twice a tile: by S, by O)
   uint64_t bar_q[8];                        // rank 0: a dim block of Q has landed in both
@@ -104,12 +104,12 @@ __device__ __forceinline__ float px_exp2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ void px_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ void px_sync() { asm volatile("bar.sync 1, 512;" ::: "memory"); }
 // Barrier of the softmax warps that returns whether any of their threads passed true.
 __device__ __forceinline__ bool px_any(bool v) {
   uint32_t r;
   asm volatile(
-      "{ .reg .pred p, q; setp.ne.b32 p, %1, 0; barrier.cta.red.or.pred q, 1, 256, p; selp.u32 %0, 1, 0, q; }"
+      "{ .reg .pred p, q; setp.ne.b32 p, %1, 0; barrier.cta.red.or.pred q, 1, 512, p; selp.u32 %0, 1, 0, q; }"
       : "=r"(r) : "r"((uint32_t)v) : "memory");
   return r != 0;
 }
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) __cluster_dims__(2, 1, 1)
     prefetch_tensormap(&kmap);
     if (P.otiles > 0) prefetch_tensormap(&omap);
   }
-  if (warp == 9) { tmem_alloc_pair(&S.tmem_base, 512); tmem_relinquish_pair(); }
+  if (warp == 17) { tmem_alloc_pair(&S.tmem_base, 512); tmem_relinquish_pair(); }
   pdl_trigger();
   __syncthreads();
   cluster_sync_all();                        // both CTAs' barriers and tensor memory are there
@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) __cluster_dims__(2, 1, 1)
   bool ok = true;
   pdl_wait();
 
-  if (warp == 8) {
+  if (warp == 16) {
     // ------------------------------------------------------------------------ TMA producer (one per CTA)
     if (lane == 0) {
       uint32_t tile = 0, part = 0;
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) __cluster_dims__(2, 1, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 9) {
+  } else if (warp == 17) {
     // ------------------------------------------------------------------------ MMA issuer
     // (the whole warp of rank 0 walks, one lane issues: see elect_one)
     if (rank == 0) {
@@ -247,12 +247,14 @@ __global__ void __launch_bounds__(PX_THREADS, 1) __cluster_dims__(2, 1, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------------------------ softmax and epilogue
-    // warp: lane quadrant `quad`, columns 64 ch .. of its lanes.  A thread has one row, and of a tile the 64 keys
-    // of quarter kq; of O the dims 128 (quad >> 1) .. of each 256.
+    // warp: lane quadrant `quad`, quarter `ch` of its lanes' columns.  A thread has one row, and of a tile the 32 keys
+    // of eighth kq.  (16 warps of 32 keys: 8 warps of 64 spilled and hid less latency.)
     const int quad = warp & 3, ch = warp >> 2;
-    const int row = 32 * (quad & 1) + lane, kq = 2 * (quad >> 1) + ch;
+    const int row = 32 * (quad & 1) + lane, kq = 4 * (quad >> 1) + ch;
     const uint32_t lane_base = tb + ((uint32_t)(32 * quad) << 16);
-    uint8_t* prow = &S.P[kq][row * 128];
+    uint8_t* prow = &S.P[kq >> 1][row * 128];
+    float (*red)[64] = reinterpret_cast<float (*)[64]>(S.P[0]);   // [key eighth][row], while P holds nothing of use
+    const int pc = 4 * (kq & 1);                 // the thread's 16-byte chunks of that row: pc .. pc + 3
     const uint32_t bar_p = peer_addr(&S.bar_p, 0);
     uint32_t f = 0, part = 0;
     for (long long g = g_begin; g < g_end; ++part) {
@@ -281,72 +283,89 @@ __global__ void __launch_bounds__(PX_THREADS, 1) __cluster_dims__(2, 1, 1)
       for (long long t = g; t < e; ++t, ++f) {
         const bool first = t == g;
         const PxTile w = px_tile(P, blk, (int)(t - blk * P.tiles));
-        const int k0 = w.key0 + 64 * kq;         // this thread's first key
+        const int k0 = w.key0 + 32 * kq;         // this thread's first key
         ok = ok && mbar_wait(&S.bar_s, f & 1);
         tc_fence_after();
-        float z[64];
-        {
-          uint32_t v[32], u[32];
-          tmem_ld_x32(lane_base + PX_COL_S + 64 * ch, v);
-          tmem_ld_x32(lane_base + PX_COL_S + 64 * ch + 32, u);
-          tmem_wait_ld_x32(v);
-          tmem_wait_ld_x32(u);
+        // The tile is done with the reference as it is; where that turns out too low for some row (every thread of the CTA
+        // learns of it at once), or in a part's first tile, once more with moved references.  The columns come 16 at a
+        // time and the loops stay rolled: unrolled over all columns the kernel outgrows the instruction caches, and a
+        // tile took a tenth longer.
+        const int e0 = w.b < 0 ? nv - k0 : w.b == b ? ve - k0 : 0;      // keys j < e0 and w0 <= j < w1 are seen
+        const int w0 = wl - k0, w1 = w.b >= 0 && w.b == b ? wh - k0 : w0;
+        const bool all = w.b < 0 && e0 >= 32;
+        auto scores = [&](int c, float (&z)[16]) -> float {             // columns 16 c ..; returns their maximum
+          uint32_t v[16];
+          tmem_ld_x16(lane_base + PX_COL_S + 32 * ch + 16 * c, v);
+          tmem_wait_ld_x16(v);
+          float top = -INFINITY;
 #pragma unroll
-          for (int j = 0; j < 32; ++j) { z[j] = __uint_as_float(v[j]); z[j + 32] = __uint_as_float(u[j]); }
-        }
-        if (w.b >= 0) {
-          const int e0 = w.b == b ? ve - k0 : 0, w0 = wl - k0, w1 = w.b == b ? wh - k0 : w0;
+          for (int j = 0; j < 16; ++j) z[j] = __uint_as_float(v[j]);
+          if (!all) {
 #pragma unroll
-          for (int j = 0; j < 64; ++j)
-            if (!(j < e0 || (j >= w0 && j < w1))) z[j] = -INFINITY;
-        } else if (k0 + 64 > nv) {
-#pragma unroll
-          for (int j = 0; j < 64; ++j)
-            if (k0 + j >= nv) z[j] = -INFINITY;
-        }
-        float top = z[0];
-#pragma unroll
-        for (int j = 1; j < 64; ++j) top = fmaxf(top, z[j]);
-        top *= P.scale_log2;                     // (the scale is positive)
-        if (first || px_any(top > m + PX_SLACK)) {
-          S.red[kq][row] = top;
-          px_sync();
-          const float mt = fmaxf(fmaxf(S.red[0][row], S.red[1][row]), fmaxf(S.red[2][row], S.red[3][row]));
-          const float mn = first || mt > m + PX_SLACK ? fmaxf(m, mt) : m;
-          const float fc = first || mn == m ? 1.f : exp2f(m - mn);
-          m = mn;
-          l *= fc;
-          if (!first && __any_sync(0xffffffffu, fc != 1.f)) {
-            // O of the rows whose reference moved (the O MMAs so far completed before S did); this thread's half of
-            // its lane's 256 columns
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              uint32_t o[32];
-              const uint32_t at = lane_base + PX_COL_O + 128 * ch + 32 * c;
-              tmem_ld_x32(at, o);
-              tmem_wait_ld_x32(o);
-#pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * fc);
-              tmem_st_x16(at, o);
-              tmem_st_x16(at + 16, o + 16);
+            for (int j = 0; j < 16; ++j) {
+              const int k = 16 * c + j;
+              if (!(k < e0 || (k >= w0 && k < w1))) z[j] = -INFINITY;
             }
-            tmem_wait_st();
           }
-          px_sync();                             // red has been read
-        }
-        const float mm = m == -INFINITY ? 0.f : m;   // (a row that sees no key: every z is -inf)
 #pragma unroll
-        for (int j = 0; j < 64; j += 8) {
-          float p[8];
+          for (int j = 0; j < 16; ++j) top = fmaxf(top, z[j]);
+          return top;
+        };
+        float lt;                                // this thread's part of the tile's sum
+        for (bool again = first;; again = true) {
+          if (again) {
+            float z[16], top = -INFINITY;
+#pragma unroll 1
+            for (int c = 0; c < 2; ++c) top = fmaxf(top, scores(c, z));
+            red[kq][row] = top * P.scale_log2;   // (the scale is positive)
+            px_sync();
+            float mt = red[0][row];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            p[i] = px_exp2(fmaf(z[j + i], P.scale_log2, -mm));
-            l += p[i];
+            for (int i = 1; i < 8; ++i) mt = fmaxf(mt, red[i][row]);
+            const float mn = first || mt > m + PX_SLACK ? fmaxf(m, mt) : m;
+            const float fc = first || mn == m ? 1.f : exp2f(m - mn);
+            m = mn;
+            l *= fc;
+            if (!first && __any_sync(0xffffffffu, fc != 1.f)) {
+              // O of the rows whose reference moved (the O MMAs so far completed before S did); this thread's
+              // quarter of its lane's 256 columns
+#pragma unroll 1
+              for (int c = 0; c < 4; ++c) {
+                uint32_t o[16];
+                const uint32_t at = lane_base + PX_COL_O + 64 * ch + 16 * c;
+                tmem_ld_x16(at, o);
+                tmem_wait_ld_x16(o);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * fc);
+                tmem_st_x16(at, o);
+              }
+              tmem_wait_st();
+            }
+            px_sync();                           // red has been read
           }
-          // P is rounded to bf16 for the MMA (2^-8 of a probability); l adds the unrounded values
-          *reinterpret_cast<uint4*>(prow + ((((j >> 3) ^ row) & 7) << 4)) =
-              make_uint4(pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]), pack_bf16x2(p[4], p[5]), pack_bf16x2(p[6], p[7]));
+          const float mm = m == -INFINITY ? 0.f : m;   // (a row that sees no key: every z is -inf)
+          float top = -INFINITY;
+          lt = 0.f;
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            float z[16];
+            top = fmaxf(top, scores(c, z));
+#pragma unroll
+            for (int j = 0; j < 16; j += 8) {
+              float p[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                p[i] = px_exp2(fmaf(z[j + i], P.scale_log2, -mm));
+                lt += p[i];
+              }
+              // P is rounded to bf16 for the MMA (2^-8 of a probability); the sum takes the unrounded values
+              *reinterpret_cast<uint4*>(prow + ((((pc + 2 * c + (j >> 3)) ^ row) & 7) << 4)) =
+                  make_uint4(pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]), pack_bf16x2(p[4], p[5]), pack_bf16x2(p[6], p[7]));
+            }
+          }
+          if (again || !px_any(top * P.scale_log2 > m + PX_SLACK)) break;
         }
+        l += lt;
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
@@ -355,48 +374,47 @@ __global__ void __launch_bounds__(PX_THREADS, 1) __cluster_dims__(2, 1, 1)
       // ---- the part's partial: O / l
       const int slot = P.slot0 + (int)(pair - px_pair_of(blk * P.tiles, G, P.T));
       const long long out = prt + (long long)slot * P.H;
-      S.red[kq][row] = l;
+      ok = ok && mbar_wait(&S.bar_o, part & 1);
+      tc_fence_after();
+      red[kq][row] = l;
       px_sync();
-      const float lt = (S.red[0][row] + S.red[1][row]) + (S.red[2][row] + S.red[3][row]);
+      float ls = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ls += red[i][row];
       px_sync();                                 // red is free again
-      const float inv = lt == 0.f ? 0.f : 1.f / lt;
+      const float inv = ls == 0.f ? 0.f : 1.f / ls;
       if (real && kq == 0) {
-        P.part_lse[out] = lt == 0.f ? -INFINITY : (m + log2f(lt)) * PX_LN2;
+        P.part_lse[out] = ls == 0.f ? -INFINITY : (m + log2f(ls)) * PX_LN2;
         // slots of this block that no pair fills
         if (e == blk_end)
           for (int s = slot + 1; s < P.slot0 + P.pslots; ++s) P.part_lse[prt + (long long)s * P.H] = -INFINITY;
       }
-      ok = ok && mbar_wait(&S.bar_o, part & 1);
-      tc_fence_after();
-      // columns 128 ch ..: dims 256 ch + 128 (quad >> 1) .., 64 at a time through this warp's 4 KB of the P buffer (the
-      // O MMAs have read it) so that 8 lanes store 128 bytes of a row (16 bytes a row and store took 6000 cycles)
-      uint8_t* stage = S.P[0] + 4096 * warp;
-      uint16_t* dst = P.part_o + 256 * ch + 128 * (quad >> 1) + 8 * (lane & 7);
+      // columns 64 ch ..: dims 256 (ch >> 1) + 128 (quad >> 1) + 64 (ch & 1) .., 32 at a time through this warp's 2 KB of
+      // the P buffer (the O MMAs have read it) so that 4 lanes store 64 bytes of a row (16 bytes a row and store took
+      // 6000 cycles)
+      uint8_t* stage = S.P[0] + 2048 * warp;
+      uint16_t* dst = P.part_o + 256 * (ch >> 1) + 128 * (quad >> 1) + 64 * (ch & 1) + 8 * (lane & 3);
 #pragma unroll 1
       for (int c = 0; c < 2; ++c) {
-        uint32_t o[2][32];
-        tmem_ld_x32(lane_base + PX_COL_O + 128 * ch + 64 * c, o[0]);
-        tmem_ld_x32(lane_base + PX_COL_O + 128 * ch + 64 * c + 32, o[1]);
-        tmem_wait_ld_x32(o[0]);
-        tmem_wait_ld_x32(o[1]);
+        uint32_t o[32];
+        tmem_ld_x32(lane_base + PX_COL_O + 64 * ch + 32 * c, o);
+        tmem_wait_ld_x32(o);
         __syncwarp();                            // the rows of the round before have been read
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < 4; ++k) {
           uint32_t w[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int j = 8 * k + 2 * i;
-            w[i] = pack_bf16x2(__uint_as_float(o[j >> 5][j & 31]) * inv, __uint_as_float(o[j >> 5][(j & 31) + 1]) * inv);
-          }
-          *reinterpret_cast<uint4*>(stage + lane * 128 + ((k ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int i = 0; i < 4; ++i)
+            w[i] = pack_bf16x2(__uint_as_float(o[8 * k + 2 * i]) * inv, __uint_as_float(o[8 * k + 2 * i + 1]) * inv);
+          *reinterpret_cast<uint4*>(stage + lane * 64 + (((k ^ (lane >> 1)) & 3) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
         __syncwarp();
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int r = 4 * k + (lane >> 3);
+        for (int k = 0; k < 4; ++k) {
+          const int r = 8 * k + (lane >> 2);
           const long long ro = __shfl_sync(0xffffffffu, real ? out : -1LL, r);
-          const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
-          if (ro >= 0) *reinterpret_cast<uint4*>(dst + ro * 512 + 64 * c) = w;
+          const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 64 + ((((lane & 3) ^ (r >> 1)) & 3) << 4));
+          if (ro >= 0) *reinterpret_cast<uint4*>(dst + ro * 512 + 32 * c) = w;
         }
       }
       tc_fence_before();
@@ -409,7 +427,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) __cluster_dims__(2, 1, 1)
   __syncthreads();
   if (S.err && tid == 0) atomicOr(&g_csa_device_error, 1u);
   cluster_sync_all();
-  if (warp == 9) {
+  if (warp == 17) {
     tc_fence_after();
     tmem_dealloc_pair(tb, 512);
   }
