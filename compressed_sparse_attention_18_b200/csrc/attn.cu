@@ -725,9 +725,9 @@ static csa_status run_attn(const csa_attn_args* a, void* ws, size_t ws_bytes, vo
                              a->out_rope_theta, st);
 }
 
-// Merge of many partials of few rows: one CTA a row, its 8 warps take the slots in turn (the merge above walks them six
+// Merge of many partials of few rows: one CTA a row, its 4 warps take the slots in turn (the merge above walks them six
 // at a time with one warp: 34 slots of 64 rows took it 16 us).
-constexpr int MERGE_WIDE_WARPS = 8, MERGE_WIDE_FROM = 7;
+constexpr int MERGE_WIDE_WARPS = 4, MERGE_WIDE_AT_ONCE = 4, MERGE_WIDE_FROM = 7;
 
 __global__ void __launch_bounds__(MERGE_WIDE_WARPS * 32)
     attn_merge_wide_kernel(const uint16_t* __restrict__ part_o, const float* __restrict__ part_lse, int slots, int H,
@@ -741,32 +741,39 @@ __global__ void __launch_bounds__(MERGE_WIDE_WARPS * 32)
   pdl_wait();
   const uint16_t* base = part_o + (bq * slots * H + h) * 512LL + lane * 16;
   const float* lrow = part_lse + bq * slots * H + h;
+  // every load of a round goes out before the weights are known; slots without keys (lse = -inf, never written) are
+  // dropped by a select, never multiplied
+  PartDims<uint16_t, 16> v[MERGE_WIDE_AT_ONCE];
+  float ls[MERGE_WIDE_AT_ONCE];
+  auto fetch = [&](int s0) {
+#pragma unroll
+    for (int c = 0; c < MERGE_WIDE_AT_ONCE; ++c) {
+      const int s = s0 + c * MERGE_WIDE_WARPS;
+      ls[c] = s < slots ? lrow[(long long)s * H] : -INFINITY;
+      if (s < slots) v[c].load(base + (long long)s * H * 512);
+    }
+  };
+  fetch(warp);
   float mx = -INFINITY, sum = 0.f;
   for (int s = lane; s < slots; s += 32) mx = fmaxf(mx, lrow[(long long)s * H]);
   mx = warp_max(mx);
   for (int s = lane; s < slots; s += 32) {
-    const float v = lrow[(long long)s * H];
-    sum += v == -INFINITY ? 0.f : exp2f((v - mx) * LOG2E);
+    const float x = lrow[(long long)s * H];
+    sum += x == -INFINITY ? 0.f : exp2f((x - mx) * LOG2E);
   }
   sum = warp_sum(sum);
   float acc[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-  for (int s0 = warp; s0 < slots; s0 += 4 * MERGE_WIDE_WARPS) {
-    PartDims<uint16_t, 16> v[4];
-    float w[4];
+  for (int s0 = warp; s0 < slots; s0 += MERGE_WIDE_AT_ONCE * MERGE_WIDE_WARPS) {
+    if (s0 != warp) fetch(s0);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int s = s0 + c * MERGE_WIDE_WARPS;
-      const float ls = s < slots ? lrow[(long long)s * H] : -INFINITY;
-      w[c] = ls == -INFINITY ? 0.f : exp2f((ls - mx) * LOG2E);      // (a slot without keys was not written)
-      if (w[c] != 0.f) v[c].load(base + (long long)s * H * 512);
+    for (int c = 0; c < MERGE_WIDE_AT_ONCE; ++c) {
+      if (ls[c] == -INFINITY) continue;
+      const float w = exp2f((ls[c] - mx) * LOG2E);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[i] = fmaf(w, v[c].get(i), acc[i]);
     }
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if (w[c] != 0.f)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[i] = fmaf(w[c], v[c].get(i), acc[i]);
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) sum_o[warp][i][lane] = make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);

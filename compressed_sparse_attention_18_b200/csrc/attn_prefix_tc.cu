@@ -67,6 +67,7 @@ struct PxParams {
   int nseq, otiles;       // own keys: sequences a block can touch, tiles of one sequence (0: attended elsewhere)
   int B, Nq, H, ratio, n_p, n_max;
   int E, Wn, window;      // own rows of a sequence: entries n_p .. n_p + E - 1, then Wn window rows
+  int early;              // the kernel before this one is own_rows_kernel: only own tiles wait for it
   const int64_t* win_pos0;
   int slot0, slots;       // partial slots of a query: this kernel's first, and all
   int pslots;             // this kernel's
@@ -142,7 +143,8 @@ __global__ void __launch_bounds__(PX_THREADS, 1) __cluster_dims__(2, 1, 1)
   tc_fence_after();
   const uint32_t tb = S.tmem_base;
   bool ok = true;
-  pdl_wait();
+  // own_rows_kernel lets this grid start only after all work before it has completed, and writes nothing but own rows
+  if (!P.early) pdl_wait();
 
   if (warp == 16) {
     // ------------------------------------------------------------------------ TMA producer (one per CTA)
@@ -156,6 +158,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) __cluster_dims__(2, 1, 1)
         for (; g < e && ok; ++g, ++tile) {
           const PxTile w = px_tile(P, blk, (int)(g - blk * P.tiles));
           const CUtensorMap* map = w.b < 0 ? &kmap : &omap;
+          if (w.b >= 0) pdl_wait();              // (again and again: a no-op after the first)
           for (int j = 0; j < 8 && ok; ++j) {
             if (tile > 0 && !mbar_wait(&S.rel[j], 1)) { ok = false; break; }      // read by the previous tile's O
             if (q_due) {
@@ -426,6 +429,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) __cluster_dims__(2, 1, 1)
   // that has left
   __syncthreads();
   if (S.err && tid == 0) atomicOr(&g_csa_device_error, 1u);
+  if (P.early && tid == 0) pdl_wait();           // the grid completes only after its predecessor
   cluster_sync_all();
   if (warp == 17) {
     tc_fence_after();
@@ -464,7 +468,14 @@ void attn_prefix_plan(const csa_attn_args* a, int n_p, bool own, int most, int* 
   if (own) px_own(a, n_p, &nseq, &otiles);
   const long long blocks = (R + PX_ROWS - 1) / PX_ROWS;
   const long long tiles = ((long long)n_p + PX_KEYS - 1) / PX_KEYS + (long long)nseq * otiles, T = blocks * tiles;
+  // Every part costs about as much as 1.2 tiles on top (its first operands from L2, its epilogue).  Cut evenly over all
+  // pairs a pair often has two parts; cut at the blocks' ends (a whole number of pairs a block) it has one, of ever so
+  // many more tiles: 16 sequences over 8192 entries, 8 blocks of 34 tiles, 37.0 us with 74 pairs, 33.1 with 72.
   long long G = T < 74 ? T : 74;
+  if (T > 74 && blocks <= 74) {
+    const long long k = 74 / blocks < tiles ? 74 / blocks : tiles;
+    if ((double)((tiles + k - 1) / k) + 1.2 < (double)T / 74 + 2.4) G = blocks * k;
+  }
   if (G > blocks * (most - 1)) G = blocks * (most - 1);    // a block is cut into at most ceil(G / blocks) + 1 parts
   long long worst = 1;
   if (blocks >= G) {
@@ -505,6 +516,7 @@ csa_status launch_attn_prefix(const csa_attn_args* a, const void* prefix, int n_
   P.ptiles = (n_p + PX_KEYS - 1) / PX_KEYS;
   if (own_rows) px_own(a, n_p, &P.nseq, &P.otiles);
   P.tiles = P.ptiles + P.nseq * P.otiles;
+  P.early = own_rows != nullptr;
   P.B = a->B; P.window = a->window; P.win_pos0 = a->win_pos0;
   P.T = (R + PX_ROWS - 1) / PX_ROWS * P.tiles;
   P.Nq = a->Nq; P.H = a->H; P.ratio = a->ratio; P.n_p = n_p; P.n_max = a->n_max;

@@ -117,8 +117,9 @@ struct OwnRowsParams {
 __global__ void __launch_bounds__(256) own_rows_kernel(const OwnRowsParams P) {
   const uint32_t r = blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  pdl_trigger();
+  // in this order: the attention behind this kernel reads inputs of earlier work as soon as it starts
   pdl_wait();
+  pdl_trigger();
   if (r >= P.total) return;
   const int b = (int)(r / P.per), u = (int)(r % P.per);
   uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
