@@ -587,7 +587,8 @@ csa_status launch_attn_tc(const csa_attn_args* a, int hca, int first, int splits
 bool attn_prefix_takes_own(const csa_attn_args* a, int n_p);
 void attn_prefix_plan(const csa_attn_args* a, int n_p, bool own, int most, int* pairs, int* slots);
 csa_status launch_attn_prefix(const csa_attn_args* a, const void* prefix, int n_p, const void* own_rows, int pairs, int slot0,
-                              int pslots, int slots, uint16_t* part_o, float* part_lse, cudaStream_t st);
+                              int pslots, int slots, uint16_t* part_o, float* part_scale, float* part_lse,
+                              cudaStream_t st);
 csa_status launch_own_rows(const csa_attn_args* a, int first, void* out, cudaStream_t st);
 
 bool attn_tc_eligible(const csa_attn_args* a, int hca, int max_splits);
@@ -725,87 +726,107 @@ static csa_status run_attn(const csa_attn_args* a, void* ws, size_t ws_bytes, vo
                              a->out_rope_theta, st);
 }
 
-// Merge of many partials of few rows: one CTA a row, its 4 warps take the slots in turn (the merge above walks them six
-// at a time with one warp: 34 slots of 64 rows took it 16 us).
-constexpr int MERGE_WIDE_WARPS = 4, MERGE_WIDE_AT_ONCE = 4, MERGE_WIDE_FROM = 7;
+// Merge of the shared-prefix attention's partials: slots before `own` hold bf16 rows (the per-query attention's), the
+// others fp16 rows times a power of two for 64 dims.  W warps take the slots of a row in turn: one while a round of loads
+// covers them, four beyond (one warp walking 34 slots of 64 rows took 16 us).  Every load of a round goes out before the
+// weights are known; slots without keys (lse = -inf, never written) are dropped by a select, never multiplied.
+constexpr int SMERGE_WARPS = 4, SMERGE_AT_ONCE = 6;
 
-__global__ void __launch_bounds__(MERGE_WIDE_WARPS * 32)
-    attn_merge_wide_kernel(const uint16_t* __restrict__ part_o, const float* __restrict__ part_lse, int slots, int H,
-                           uint16_t* __restrict__ out, float* __restrict__ lse, const int64_t* __restrict__ q_pos,
-                           float rope_theta) {
-  __shared__ float4 sum_o[MERGE_WIDE_WARPS][4][32];
+template <int W>
+__global__ void __launch_bounds__(SMERGE_WARPS * 32)
+    attn_shared_merge_kernel(const uint16_t* __restrict__ part_o, const float* __restrict__ part_scale,
+                             const float* __restrict__ part_lse, int own, int slots, int H, long long units,
+                             uint16_t* __restrict__ out, float* __restrict__ lse, const int64_t* __restrict__ q_pos,
+                             float rope_theta) {
+  __shared__ float4 sum_o[W > 1 ? W : 1][4][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long bq = blockIdx.x / H;
-  const int h = (int)(blockIdx.x % H);
+  const long long unit = W > 1 ? (long long)blockIdx.x : (long long)blockIdx.x * SMERGE_WARPS + warp;
+  const int w0 = W > 1 ? warp : 0;
   pdl_trigger();
   pdl_wait();
-  const uint16_t* base = part_o + (bq * slots * H + h) * 512LL + lane * 16;
-  const float* lrow = part_lse + bq * slots * H + h;
-  // every load of a round goes out before the weights are known; slots without keys (lse = -inf, never written) are
-  // dropped by a select, never multiplied
-  PartDims<uint16_t, 16> v[MERGE_WIDE_AT_ONCE];
-  float ls[MERGE_WIDE_AT_ONCE];
+  if (unit >= units) return;                     // (W > 1: every unit has a CTA)
+  const long long bq = unit / H, row0 = bq * slots * H + unit % H;
+  uint4 v[SMERGE_AT_ONCE][2];
+  float ls[SMERGE_AT_ONCE], sc[SMERGE_AT_ONCE];
   auto fetch = [&](int s0) {
 #pragma unroll
-    for (int c = 0; c < MERGE_WIDE_AT_ONCE; ++c) {
-      const int s = s0 + c * MERGE_WIDE_WARPS;
-      ls[c] = s < slots ? lrow[(long long)s * H] : -INFINITY;
-      if (s < slots) v[c].load(base + (long long)s * H * 512);
+    for (int c = 0; c < SMERGE_AT_ONCE; ++c) {
+      const int s = s0 + c * W;
+      ls[c] = -INFINITY;
+      if (s < slots) {
+        const long long r = row0 + (long long)s * H;
+        ls[c] = part_lse[r];
+        sc[c] = s < own ? 0.f : part_scale[r * 8 + (lane >> 2)];
+        v[c][0] = reinterpret_cast<const uint4*>(part_o + r * 512 + lane * 16)[0];
+        v[c][1] = reinterpret_cast<const uint4*>(part_o + r * 512 + lane * 16)[1];
+      }
     }
   };
-  fetch(warp);
+  fetch(w0);
   float mx = -INFINITY, sum = 0.f;
-  for (int s = lane; s < slots; s += 32) mx = fmaxf(mx, lrow[(long long)s * H]);
+  for (int s = lane; s < slots; s += 32) mx = fmaxf(mx, part_lse[row0 + (long long)s * H]);
   mx = warp_max(mx);
   for (int s = lane; s < slots; s += 32) {
-    const float x = lrow[(long long)s * H];
+    const float x = part_lse[row0 + (long long)s * H];
     sum += x == -INFINITY ? 0.f : exp2f((x - mx) * LOG2E);
   }
   sum = warp_sum(sum);
   float acc[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-  for (int s0 = warp; s0 < slots; s0 += MERGE_WIDE_AT_ONCE * MERGE_WIDE_WARPS) {
-    if (s0 != warp) fetch(s0);
+  for (int s0 = w0; s0 < slots; s0 += SMERGE_AT_ONCE * W) {
+    if (s0 != w0) fetch(s0);
 #pragma unroll
-    for (int c = 0; c < MERGE_WIDE_AT_ONCE; ++c) {
+    for (int c = 0; c < SMERGE_AT_ONCE; ++c) {
       if (ls[c] == -INFINITY) continue;
       const float w = exp2f((ls[c] - mx) * LOG2E);
+      const bool bf = s0 + c * W < own;
+      const float f = bf ? w : w * sc[c];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) acc[i] = fmaf(w, v[c].get(i), acc[i]);
+      for (int i = 0; i < 8; ++i) {
+        const uint4 q = v[c][i >> 2];
+        const uint32_t x = (i & 3) == 0 ? q.x : (i & 3) == 1 ? q.y : (i & 3) == 2 ? q.z : q.w;
+        const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&x));
+        acc[2 * i] = fmaf(f, bf ? __uint_as_float(x << 16) : h.x, acc[2 * i]);
+        acc[2 * i + 1] = fmaf(f, bf ? __uint_as_float(x & 0xFFFF0000u) : h.y, acc[2 * i + 1]);
+      }
     }
   }
+  if (W > 1) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) sum_o[warp][i][lane] = make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
-  __syncthreads();
-  if (warp != 0) return;
+    for (int i = 0; i < 4; ++i) sum_o[warp][i][lane] = make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+    __syncthreads();
+    if (warp != 0) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int r = 1; r < W; ++r) {
+        const float4 u = sum_o[r][i][lane];
+        acc[4 * i] += u.x; acc[4 * i + 1] += u.y; acc[4 * i + 2] += u.z; acc[4 * i + 3] += u.w;
+      }
+  }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float4 t = sum_o[0][i][lane];
-#pragma unroll
-    for (int r = 1; r < MERGE_WIDE_WARPS; ++r) {
-      const float4 u = sum_o[r][i][lane];
-      t.x += u.x; t.y += u.y; t.z += u.z; t.w += u.w;
-    }
-    acc[4 * i] = t.x * inv; acc[4 * i + 1] = t.y * inv; acc[4 * i + 2] = t.z * inv; acc[4 * i + 3] = t.w * inv;
-  }
+  for (int i = 0; i < 16; ++i) acc[i] *= inv;
   if (rope_theta != 0.f) inverse_rope_lanes<512>(acc, lane, q_pos[bq], rope_theta);
   uint32_t pk[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) pk[i] = pack_bf16x2(acc[2 * i], acc[2 * i + 1]);
-  uint4* o = reinterpret_cast<uint4*>(out + (bq * H + h) * 512LL + lane * 16);
+  uint4* o = reinterpret_cast<uint4*>(out + unit * 512 + lane * 16);
   o[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
   o[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
-  if (lse && lane == 0) lse[bq * H + h] = sum == 0.f ? -INFINITY : mx + logf(sum);
+  if (lse && lane == 0) lse[unit] = sum == 0.f ? -INFINITY : mx + logf(sum);
 }
 
-static csa_status launch_merge_wide(const uint16_t* po, const float* pl, int slots, int H, long long rows, uint16_t* out,
-                                    float* lse, const int64_t* q_pos, float rope_theta, cudaStream_t st) {
+template <int W>
+static csa_status launch_shared_merge(const uint16_t* po, const float* ps, const float* pl, int own, int slots, int H,
+                                      long long rows, uint16_t* out, float* lse, const int64_t* q_pos, float rope_theta,
+                                      cudaStream_t st) {
   static std::atomic<unsigned> attr_done{0};
-  set_smem_once((const void*)attn_merge_wide_kernel, 0, attr_done);
-  return launch_pdl(attn_merge_wide_kernel, dim3((unsigned)(rows * H)), dim3(MERGE_WIDE_WARPS * 32), 0, st, po, pl, slots, H,
-                    out, lse, q_pos, rope_theta);
+  set_smem_once((const void*)attn_shared_merge_kernel<W>, 0, attr_done);
+  const long long units = rows * H, grid = W > 1 ? units : (units + SMERGE_WARPS - 1) / SMERGE_WARPS;
+  return launch_pdl(attn_shared_merge_kernel<W>, dim3((unsigned)grid), dim3(SMERGE_WARPS * 32), 0, st, po, ps, pl, own, slots,
+                    H, units, out, lse, q_pos, rope_theta);
 }
 
 // ---- HCA with a shared prefix: the prefix by attn_prefix_tc_kernel, the sequences' own keys (entries from n_p on, and
@@ -814,7 +835,7 @@ struct SharedPlan {
   int own, tpc;           // splits of the own keys in the per-query attention (0: not there), their tiles per CTA
   bool rows;              // own keys in the prefix kernel
   int pairs, pslots;      // the prefix kernel's
-  size_t off_lse, off_rows, total;
+  size_t off_scale, off_lse, off_rows, total;
 };
 
 static SharedPlan plan_shared(const csa_shared_attn_args* s) {
@@ -825,7 +846,8 @@ static SharedPlan plan_shared(const csa_shared_attn_args* s) {
   if (own > 0 && !p.rows) attn_tc_plan(a, 1, s->n_prefix, &p.own, &p.tpc);
   attn_prefix_plan(a, s->n_prefix, p.rows, MERGE_MAX_SPLITS, &p.pairs, &p.pslots);
   const size_t parts = (size_t)a->B * a->Nq * (p.own + p.pslots) * a->H;
-  p.off_lse = align_up(parts * 512 * 2, 256);
+  p.off_scale = align_up(parts * 512 * 2, 256);
+  p.off_lse = align_up(p.off_scale + parts * 8 * 4, 256);
   p.off_rows = align_up(p.off_lse + parts * 4, 256);
   p.total = p.off_rows + (p.rows ? (size_t)a->B * own * 1024 : 0);
   return p;
@@ -857,6 +879,7 @@ static csa_status run_shared(const csa_shared_attn_args* s, void* ws, size_t ws_
   if (ws_bytes < p.total) return CSA_ERR_WORKSPACE;
   CSA_REQUIRE(ws != nullptr);
   uint16_t* po = (uint16_t*)ws;
+  float* ps = (float*)((uint8_t*)ws + p.off_scale);
   float* pl = (float*)((uint8_t*)ws + p.off_lse);
   const int slots = p.own + p.pslots;
   void* own_rows = p.rows ? (uint8_t*)ws + p.off_rows : nullptr;
@@ -864,11 +887,10 @@ static csa_status run_shared(const csa_shared_attn_args* s, void* ws, size_t ws_
   if (p.rows) r = launch_own_rows(a, s->n_prefix, own_rows, st);
   if (p.own > 0) r = launch_attn_tc(a, 1, s->n_prefix, p.own, slots, p.tpc, po, pl, st);
   if (r == CSA_OK)
-    r = launch_attn_prefix(a, s->prefix_kv, s->n_prefix, own_rows, p.pairs, p.own, p.pslots, slots, po, pl, st);
+    r = launch_attn_prefix(a, s->prefix_kv, s->n_prefix, own_rows, p.pairs, p.own, p.pslots, slots, po, ps, pl, st);
   if (r != CSA_OK) return r;
-  if (slots >= MERGE_WIDE_FROM)
-    return launch_merge_wide(po, pl, slots, a->H, rows, (uint16_t*)a->out, a->lse, a->q_pos, a->out_rope_theta, st);
-  return launch_merge<uint16_t>(po, pl, slots, a->H, a->d, rows, (uint16_t*)a->out, a->lse, a->q_pos, a->out_rope_theta, st);
+  return (slots <= SMERGE_AT_ONCE ? launch_shared_merge<1> : launch_shared_merge<SMERGE_WARPS>)(
+      po, ps, pl, p.own, slots, a->H, rows, (uint16_t*)a->out, a->lse, a->q_pos, a->out_rope_theta, st);
 }
 
 }  // namespace csa

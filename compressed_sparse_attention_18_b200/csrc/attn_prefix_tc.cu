@@ -26,7 +26,8 @@
 // A block's last tiles can be the own keys of the sequences it touches (bf16 rows from own_rows_kernel), masked to the rows
 // of their sequence and to what each sees.
 // Parts: the tiles of all blocks of 128 rows form one line that is cut evenly over the pairs, so a pair works on the end
-// of one block and the start of the next, and each leaves a partial (O / l in bf16, lse) that the split merge adds.
+// of one block and the start of the next, and each leaves a partial (O / l in scaled fp16, lse) that the
+// merge adds.
 // Every wait is bounded; a wait that gives up records device error 1 and the kernel leaves.
 // Sources: "DeepSeek-V4: エージェントが実際に使える100万トークンのコンテキスト", §ハイブリッド注意, Fig. 4 (the 128x layer
 // attends densely over all visible entries).
@@ -74,7 +75,8 @@ struct PxParams {
   float scale_log2;
   const int64_t* q_pos;
   const int32_t* n_c;
-  uint16_t* part_o;       // [query][slots][H][512] bf16
+  uint16_t* part_o;       // [query][slots][H][512] fp16, times
+  float* part_scale;      // [query][slots][H][8]: a power of two for 64 dims
   float* part_lse;        // [query][slots][H]
 };
 
@@ -392,11 +394,26 @@ __global__ void __launch_bounds__(PX_THREADS, 1) __cluster_dims__(2, 1, 1)
         if (e == blk_end)
           for (int s = slot + 1; s < P.slot0 + P.pslots; ++s) P.part_lse[prt + (long long)s * P.H] = -INFINITY;
       }
-      // columns 64 ch ..: dims 256 (ch >> 1) + 128 (quad >> 1) + 64 (ch & 1) .., 32 at a time through this warp's 2 KB of
-      // the P buffer (the O MMAs have read it) so that 4 lanes store 64 bytes of a row (16 bytes a row and store took
-      // 6000 cycles)
+      // This thread's columns 64 ch .. are the dims 64 blk64 .. of its row: fp16 values times a power of two for the 64
+      // (from their largest), 2^-12 off at most where bf16 would be 2^-9, at no more bytes.
+      const int blk64 = 4 * (ch >> 1) + 2 * (quad >> 1) + (ch & 1);
+      float big = 0.f;
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t o[16];
+        tmem_ld_x16(lane_base + PX_COL_O + 64 * ch + 16 * c, o);
+        tmem_wait_ld_x16(o);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) big = fmaxf(big, fabsf(__uint_as_float(o[j])));
+      }
+      const uint32_t ex = min(max(__float_as_uint(big * inv) >> 23, 1u), 253u);
+      const bool finite = big * inv < INFINITY;
+      const float fac = finite ? inv * __uint_as_float((254u - ex) << 23) : inv;
+      if (real) P.part_scale[out * 8 + blk64] = finite ? __uint_as_float(ex << 23) : 1.f;
+      // 32 columns at a time through this warp's 2 KB of the P buffer (the O MMAs have read it) so that 4 lanes store 64
+      // bytes of a row (16 bytes a row and store took 6000 cycles)
       uint8_t* stage = S.P[0] + 2048 * warp;
-      uint16_t* dst = P.part_o + 256 * (ch >> 1) + 128 * (quad >> 1) + 64 * (ch & 1) + 8 * (lane & 3);
+      uint16_t* dst = P.part_o + 64 * blk64 + 8 * (lane & 3);
 #pragma unroll 1
       for (int c = 0; c < 2; ++c) {
         uint32_t o[32];
@@ -407,8 +424,10 @@ __global__ void __launch_bounds__(PX_THREADS, 1) __cluster_dims__(2, 1, 1)
         for (int k = 0; k < 4; ++k) {
           uint32_t w[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            w[i] = pack_bf16x2(__uint_as_float(o[8 * k + 2 * i]) * inv, __uint_as_float(o[8 * k + 2 * i + 1]) * inv);
+          for (int i = 0; i < 4; ++i) {
+            const __half2 h = __floats2half2_rn(__uint_as_float(o[8 * k + 2 * i]) * fac, __uint_as_float(o[8 * k + 2 * i + 1]) * fac);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+          }
           *reinterpret_cast<uint4*>(stage + lane * 64 + (((k ^ (lane >> 1)) & 3) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
         __syncwarp();
@@ -492,7 +511,8 @@ void attn_prefix_plan(const csa_attn_args* a, int n_p, bool own, int most, int* 
 
 // own_rows: own_rows_kernel's output, or null (the own keys are attended elsewhere).
 csa_status launch_attn_prefix(const csa_attn_args* a, const void* prefix, int n_p, const void* own_rows, int pairs, int slot0,
-                              int pslots, int slots, uint16_t* part_o, float* part_lse, cudaStream_t st) {
+                              int pslots, int slots, uint16_t* part_o, float* part_scale, float* part_lse,
+                              cudaStream_t st) {
   const long long R = (long long)a->B * a->Nq * a->H;
   CUtensorMap qm, km, om;
   auto encode = [](CUtensorMap* map, const void* base, long long rows, int box) {
@@ -522,7 +542,7 @@ csa_status launch_attn_prefix(const csa_attn_args* a, const void* prefix, int n_
   P.Nq = a->Nq; P.H = a->H; P.ratio = a->ratio; P.n_p = n_p; P.n_max = a->n_max;
   P.slot0 = slot0; P.slots = slots; P.pslots = pslots;
   P.scale_log2 = (a->softmax_scale != 0.0f ? a->softmax_scale : 1.0f / sqrtf(512.0f)) * PX_LOG2E;
-  P.q_pos = a->q_pos; P.n_c = a->n_c; P.part_o = part_o; P.part_lse = part_lse;
+  P.q_pos = a->q_pos; P.n_c = a->n_c; P.part_o = part_o; P.part_scale = part_scale; P.part_lse = part_lse;
   const int smem = (int)sizeof(PxSmem) + 1024;
   static_assert(sizeof(PxSmem) + 1024 <= 232448, "shared memory of a CTA");
   static std::atomic<unsigned> attr_done{0};

@@ -64,7 +64,7 @@ def test_workspace_sizes(csa):
     size = lambda **kw: csa._lib.csa_shared_attn_workspace_size(ctypes.byref(args(csa, **kw)))  # noqa: E731
     assert size() > 2 * 16 * 512 * 2 and size(B=0) == 0 and size(n_prefix=-1) == 0
     # as many partials as CTAs that share a block of rows: with one block of rows every tile has its own
-    row = 2 * 16 * (512 * 2 + 4)
+    row = 2 * 16 * (512 * 2 + 8 * 4 + 4)
     assert size(n_prefix=700, n_max=700) >= 3 * row
     assert size(n_prefix=700, n_max=700) < 4 * row
     # the own keys' partials come on top
