@@ -532,6 +532,8 @@ def hca_shared_attn(q, q_pos, cache, n_c, prefix_kv, win_kv=None, win_pos0=None,
         _need(out, "hca_shared_attn out", torch.bfloat16, tuple(q.shape), q)
     if lse is not None:
         _need(lse, "hca_shared_attn lse", torch.float32, (B, Nq, H), q)
+    if ws is not None and ws.device != q.device:
+        raise CSAError(f"hca_shared_attn ws: on {ws.device}, the other operands are on {q.device}")
     return _launch(q, stream, _shared_call, q, q_pos, cache, n_c, prefix_kv, win_kv, win_pos0, ratio, window,
                    softmax_scale, out, lse, ws, out_rope_theta)
 

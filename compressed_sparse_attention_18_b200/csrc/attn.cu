@@ -878,6 +878,7 @@ static csa_status run_shared(const csa_shared_attn_args* s, void* ws, size_t ws_
   const SharedPlan p = plan_shared(s);
   if (ws_bytes < p.total) return CSA_ERR_WORKSPACE;
   CSA_REQUIRE(ws != nullptr);
+  CSA_SUPPORTED(((uintptr_t)ws & 15) == 0);
   uint16_t* po = (uint16_t*)ws;
   float* ps = (float*)((uint8_t*)ws + p.off_scale);
   float* pl = (float*)((uint8_t*)ws + p.off_lse);

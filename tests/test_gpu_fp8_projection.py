@@ -44,6 +44,30 @@ def test_quant_bit_exact(cuda_lib, rows, K, block):
     assert np.array_equal(codes, rc)
 
 
+@pytest.mark.parametrize("exponent", [-126, -70, -55, 0, 60, 75, 126])
+def test_quant_every_mantissa_by_every_mantissa(cuda_lib, exponent):
+    """Blocks whose largest value has each of the 128 bf16 mantissas, over all mantissas and twelve binades below it: the
+    quotients fall on both sides of, and on, every rounding border of E4M3.  Scales inside and outside the range
+    where the quotient is computed with a reciprocal, and scales that are subnormal."""
+    lead = (1 + torch.arange(128) / 128.0) * 2.0 ** exponent
+    tail = (1 + torch.arange(128) / 128.0)[:, None] * 2.0 ** (exponent - 0.0 - torch.arange(12))[None, :]
+    tail = tail.reshape(-1)                                                   # 1536 values
+    blocks = []
+    for a in lead:
+        v = torch.where(tail <= a, tail, tail / 2)
+        v = torch.nn.functional.pad(v, (0, -len(v) % 127)).reshape(-1, 127)
+        blocks.append(torch.cat([a.expand(len(v), 1), v * torch.where(torch.arange(127) % 3 == 0, -1.0, 1.0)], 1))
+    x = torch.cat(blocks).to(torch.bfloat16)
+    _, codes, scales = quantised(cuda_lib, x, 1)
+    x64 = f64(x)
+    s = (np.abs(x64).max(1).astype(np.float32) / np.float32(448.0))
+    q = (x64.astype(np.float32) / s[:, None]).astype(np.float64)
+    v = O.e4m3_rne_satfinite(q)
+    want = O.e4m3_encode(np.abs(v)) | np.where(v < 0, 0x80, 0).astype(np.uint8)
+    assert np.array_equal(scales[:, 0], s.astype(np.float64))
+    assert np.array_equal(codes, want)
+
+
 @pytest.mark.parametrize("block", [1, 128])
 def test_quant_special_values(cuda_lib, block):
     """Zero blocks, -0, the type's smallest and largest values, values that all fall on E4M3 midpoints, infinities and
@@ -75,7 +99,9 @@ def test_quant_special_values(cuda_lib, block):
 # one token; each arrangement's edges; rows, channels and K that end inside a tile; parts of K of different length
 SIZES = [(1, 8, 16, False), (1, 512, 4096, True), (16, 128, 1024, True), (17, 136, 144, False), (32, 640, 1152, True),
          (33, 200, 272, True), (64, 1024, 896, False), (65, 264, 128, False), (100, 648, 2064, True), (128, 128, 1920, False),
-         (129, 8, 4096, True), (257, 1032, 272, True), (700, 1000, 784, False), (2500, 1288, 400, True)]
+         (129, 8, 4096, True), (257, 1032, 272, True), (700, 1000, 784, False), (2500, 1288, 400, True),
+         # pairs of CTAs: one block of K or a part of one, more tiles than pairs, the last tile almost empty
+         (2500, 1000, 128, True), (2305, 1040, 16, True), (5000, 2056, 144, False)]
 
 
 @pytest.mark.parametrize("M,N,K,pair", SIZES)

@@ -183,6 +183,8 @@ def test_workspace_contents_and_repeats(cuda_lib):
         assert (o2[5] == 5.0).all() and (l2[5] == 5.0).all() and (ws[n:] == fill).all()
     with pytest.raises(csa.CSAError, match="CSA_ERR_WORKSPACE"):
         csa.hca_shared_attn(*c.args, ratio=c.r, window=W, ws=ws[: n - 1])
+    with pytest.raises(csa.CSAError, match="CSA_ERR_UNSUPPORTED"):
+        csa.hca_shared_attn(*c.args, ratio=c.r, window=W, ws=ws[8: 8 + n])
 
 
 def test_captured_and_replayed(cuda_lib):
@@ -203,6 +205,33 @@ def test_captured_and_replayed(cuda_lib):
     c.prefix.copy_(d.prefix), c.win.copy_(d.win), c.win_pos0.copy_(d.win_pos0)
     g.replay()
     d.check(out, lse)
+    csa.device_status()
+
+
+def test_two_graphs_and_an_eager_call_interleaved(cuda_lib):
+    """Two captured calls of different sizes, and eager calls of both between their replays on two streams: each keeps its
+    workspace, so each result stays its own."""
+    csa = cuda_lib
+    cs = [Case(csa, 4, 1, 16, 500, 30, seed=5), Case(csa, 2, 5, 64, 1300, 90, seed=6)]
+    want = [c.run(csa) for c in cs]
+    streams, graphs, outs = [torch.cuda.Stream() for _ in cs], [], []
+    for c, s in zip(cs, streams):
+        s.wait_stream(torch.cuda.current_stream())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            outs.append(csa.hca_shared_attn(*c.args, ratio=c.r, window=W))
+        graphs.append(g)
+    for _ in range(3):
+        eager = []
+        for c, s, g in zip(cs, streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+                eager.append(csa.hca_shared_attn(*c.args, ratio=c.r, window=W))
+        for s in streams:
+            s.synchronize()
+        for got in (outs, eager):
+            for (o, l), (wo, wl) in zip(got, want):
+                assert torch.equal(o, wo) and torch.equal(l, wl)
     csa.device_status()
 
 
