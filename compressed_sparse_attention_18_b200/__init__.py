@@ -166,11 +166,9 @@ def _check(status: int, what: str):
 def _ptr(t):
     if t is None:
         return None
-    if not t.is_cuda:
-        raise CSAError("tensor is not on a CUDA device (no CPU path)")
-    if not t.is_contiguous():
-        raise CSAError("tensor must be contiguous")
-    return t.data_ptr()
+    if t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    raise CSAError("tensor must be contiguous" if t.is_cuda else "tensor is not on a CUDA device (no CPU path)")
 
 
 def _stream(stream):
@@ -190,8 +188,9 @@ def _need(t, what, dtype, shape=None, like=None):
     """Check one tensor argument of a call: its type, its shape (None: any size) and that it is on `like`'s device."""
     if not isinstance(t, torch.Tensor) or t.dtype != dtype:
         raise CSAError(f"{what}: a {dtype} tensor is needed")
-    if shape is not None and (t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape))):
-        raise CSAError(f"{what}: shape {tuple(t.shape)}, expected {tuple('any' if w is None else w for w in shape)}")
+    if shape is not None and t.shape != shape:
+        if t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape)):
+            raise CSAError(f"{what}: shape {tuple(t.shape)}, expected {tuple('any' if w is None else w for w in shape)}")
     if like is not None and t.device != like.device:
         raise CSAError(f"{what}: on {t.device}, the other operands are on {like.device}")
 
@@ -487,10 +486,9 @@ def attn_kernel_count(q, q_pos, cache, n_c, idx, win_kv, win_pos0, *, ratio, win
 
 def _shared_args(q, q_pos, cache, n_c, prefix_kv, win_kv, win_pos0, ratio, window, softmax_scale, out, lse,
                  out_rope_theta):
-    a = SharedAttnArgs(ctypes.sizeof(SharedAttnArgs), prefix_kv.shape[0], _ptr(prefix_kv))
-    a.attn = _attn_args(q, q_pos, cache, n_c, None, win_kv, win_pos0, ratio, window, softmax_scale, out, lse)
-    a.attn.out_rope_theta = out_rope_theta
-    return a
+    t = _attn_args(q, q_pos, cache, n_c, None, win_kv, win_pos0, ratio, window, softmax_scale, out, lse)
+    t.out_rope_theta = out_rope_theta
+    return SharedAttnArgs(ctypes.sizeof(SharedAttnArgs), prefix_kv.shape[0], _ptr(prefix_kv), t)
 
 
 def _shared_call(st, q, q_pos, cache, n_c, prefix_kv, win_kv, win_pos0, ratio, window, softmax_scale, out, lse, ws,
