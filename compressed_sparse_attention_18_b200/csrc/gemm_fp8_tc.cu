@@ -408,25 +408,34 @@ __global__ void __launch_bounds__(GF_THREADS, 1) __cluster_dims__(2, 1, 1)
   } else if (warp == 9 || warp == 10) {
     // ------------------------------------------------------------------------ MMA issuers (even CTA)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       const uint32_t idesc = idesc_e4m3(2 * GF_ROWS, BN);
       const uint64_t ad0 = smem_desc(smem_addr(S.a[0]), 16, 1024, LAYOUT_SW128);
       const uint64_t bd0 = smem_desc(smem_addr(S.b[0]), 16, 1024, LAYOUT_SW128);
       const int ntile = t0 < P.tiles ? (P.tiles - 1 - t0) / tstep + 1 : 0;
       const long long n = (long long)ntile * KB;
-      for (long long it = warp - 9; it < n; it += 2) {
-        const int s = (int)(it % ST), a = (int)(it % NB);
-        if (it >= NB && !mbar_wait(&S.acc_empty[a], (uint32_t)(it / NB - 1) & 1)) { ok = false; break; }
-        if (!mbar_wait(&S.full[s], (uint32_t)(it / ST) & 1)) { ok = false; break; }
+      uint32_t s = warp - 9, sph = 0;            // stage and its round
+      uint32_t aph = 0;                          // round of this thread's accumulator (NB = 2: one each)
+      for (long long it = warp - 9; it < n && ok; it += 2) {
+        const int a = warp - 9;
+        if (aph > 0 && !mbar_test(&S.acc_empty[a], (aph - 1) & 1)) ok = mbar_wait(&S.acc_empty[a], (aph - 1) & 1);
+        if (!mbar_test(&S.full[s], sph)) ok = ok && mbar_wait(&S.full[s], sph);
         tc_fence_after();
         const uint64_t ad = ad0 + (uint64_t)(s * (Cfg::A_BYTES >> 4)), bd = bd0 + (uint64_t)(s * (Cfg::B_BYTES >> 4));
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < GF_BK / 32; ++kk)
-          mma_f8_ss_pair(tbase + (uint32_t)(a * BN), ad + kk * 2, bd + kk * 2, idesc, kk != 0);
-        mma_commit_pair(&S.mma[s]);
+          for (int kk = 0; kk < GF_BK / 32; ++kk)
+            mma_f8_ss_pair(tbase + (uint32_t)(a * BN), ad + kk * 2, bd + kk * 2, idesc, kk != 0);
+          mma_commit_pair(&S.mma[s]);
+        }
+        __syncwarp();
+        ++aph;
+        s += 2;
+        if (s >= ST) { s -= ST; sph ^= 1; }
       }
-      mma_commit_pair(&S.done);
-      if (!ok) atomicOr(&S.err, 1u);
+      if (elect_one()) mma_commit_pair(&S.done);
+      __syncwarp();
+      if (!ok && lane == 0) atomicOr(&S.err, 1u);
     }
     __syncwarp();
   } else if (warp < 8) {
