@@ -5,7 +5,8 @@
 //   codes 0 (the rule of the FP8 window rows, with 128 channels to a block).  A NaN has no part in amax and
 //   becomes the NaN code; an infinity makes the scale infinite, itself NaN and the block's other codes 0.
 //
-// Bound by HBM: 2 bytes read and 1 written an element.  A block is kept in registers between its maximum and
+// Bound by HBM: 2 bytes read and 1 written an element (4096 x 4096: 10.9 us, 4.6 TB/s), with the instructions of the
+// quotients close behind (14 an element, 68 % of the issue slots).  A block is kept in registers between its maximum and
 // its codes, so the source is read once.
 #include "csa_common.cuh"
 
@@ -30,21 +31,31 @@ __device__ __forceinline__ Q8Div q8_div(float sc) {
   return d;
 }
 
-// Four E4M3 bytes of fp32(x_e / s), -0 as +0.
-__device__ __forceinline__ uint32_t q8_codes4(const float* x, const Q8Div& d) {
-  float q[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float y = x[e] * d.r;
-    q[e] = d.fast ? __fmaf_rn(d.r, __fmaf_rn(-y, d.s, x[e]), y) : __fdiv_rn(x[e], d.s);
-  }
+// Four E4M3 bytes, -0 as +0.
+__device__ __forceinline__ uint32_t q8_pack4(float a, float b, float c, float d) {
   uint16_t lo, hi;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(q[1]), "f"(q[0]));
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(q[3]), "f"(q[2]));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
   const uint32_t w = (uint32_t)lo | ((uint32_t)hi << 16);
   // a byte keeps its sign bit only if its magnitude is not 0
   const uint32_t m = w & 0x7F7F7F7Fu;
   return w & (m | (m + 0x7F7F7F7Fu));
+}
+
+// E4M3 bytes of fp32(x_e / s), 8 elements to a uint2.
+__device__ __forceinline__ uint2 q8_codes8(const float* x, const Q8Div& d) {
+  float q[8];
+  if (d.fast) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float y = x[e] * d.r;
+      q[e] = __fmaf_rn(d.r, __fmaf_rn(-y, d.s, x[e]), y);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) q[e] = __fdiv_rn(x[e], d.s);
+  }
+  return make_uint2(q8_pack4(q[0], q[1], q[2], q[3]), q8_pack4(q[4], q[5], q[6], q[7]));
 }
 
 __device__ __forceinline__ void q8_unpack(const uint4& v, float* x) {
@@ -64,8 +75,9 @@ __device__ __forceinline__ float q8_amax8(const float* x) {
 }
 
 // Rows: 8 lanes take one block of one row, two vectors of 8 elements (16 bytes) each.  EVEN (K a multiple of 128): the
-// blocks of all rows follow one another, block u at element 128 u.  4096 x 4096: 11.8 us, 4.3 TB/s; two blocks a lane
-// in flight 12.9, four 16.6 (fewer warps fit), 16 lanes a block 14.7 (the scale's two divisions are paid by each lane).
+// blocks of all rows follow one another, block u at element 128 u.  Two blocks a lane
+// in flight take a tenth longer, four half as long again (fewer warps fit), 16 lanes a block a quarter (the scale's two
+// divisions are paid by each lane).
 template <bool EVEN>
 __global__ void __launch_bounds__(256) quant_rows_kernel(const uint16_t* __restrict__ src, long long total, int K, int KB,
                                                          uint8_t* __restrict__ codes, float* __restrict__ scales) {
@@ -95,9 +107,9 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const uint16_t* __restr
   for (int o = 4; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   const float sc = __fdiv_rn(amax, 448.0f);
   const Q8Div d = q8_div(sc);
-  if (at >= 0) *reinterpret_cast<uint2*>(codes + at) = make_uint2(q8_codes4(x, d), q8_codes4(x + 4, d));
+  if (at >= 0) *reinterpret_cast<uint2*>(codes + at) = q8_codes8(x, d);
   if (at >= 0 && left > 64)
-    *reinterpret_cast<uint2*>(codes + at + 64) = make_uint2(q8_codes4(x + 8, d), q8_codes4(x + 12, d));
+    *reinterpret_cast<uint2*>(codes + at + 64) = q8_codes8(x + 8, d);
   if (sub == 0 && u < total) scales[u] = sc;
 }
 
@@ -140,7 +152,7 @@ __global__ void __launch_bounds__(Q8_BLOCK * Q8_BLOCK / 8 / VEC) quant_blocks_ke
     if (r0 + STEP * i >= rows || k0 >= K) continue;
     float x[8];
     q8_unpack(v[i], x);
-    *reinterpret_cast<uint2*>(codes + (r0 + STEP * i) * K + k0) = make_uint2(q8_codes4(x, d), q8_codes4(x + 4, d));
+    *reinterpret_cast<uint2*>(codes + (r0 + STEP * i) * K + k0) = q8_codes8(x, d);
   }
 }
 
@@ -180,8 +192,8 @@ extern "C" csa_status csa_quant_fp8(const csa_quant_fp8_args* a, void* stream) {
   const long long KB = (a->K + Q8_BLOCK - 1) / Q8_BLOCK;
   const long long blocks = ((long long)a->rows + Q8_BLOCK - 1) / Q8_BLOCK * KB;
   CSA_SUPPORTED(blocks <= 0x7fffffffLL);
-  // 1024 threads a block while one wave takes them all (the shortest chain: 1000 x 2064 in 2.8 us, 3.8 with 512), 512
-  // beyond (4096 x 4096 in 16.7 us, 3.0 TB/s; 23.4 with 1024, 17.8 with 256)
+  // 1024 threads a block while one wave takes them all (the shortest chain: 1000 x 2064 in 2.6 us, 3.8 with 512), 512
+  // beyond (4096 x 4096 in 15.3 us, 3.3 TB/s; 23.4 with 1024, 17.8 with 256)
   return blocks <= 2 * 148 ? launch_quant_blocks<2>(a, (unsigned)blocks, (cudaStream_t)stream)
                            : launch_quant_blocks<4>(a, (unsigned)blocks, (cudaStream_t)stream);
 }
