@@ -849,7 +849,8 @@ static SharedPlan plan_shared(const csa_shared_attn_args* s) {
   p.off_scale = align_up(parts * 512 * 2, 256);
   p.off_lse = align_up(p.off_scale + parts * 8 * 4, 256);
   p.off_rows = align_up(p.off_lse + parts * 4, 256);
-  p.total = p.off_rows + (p.rows ? (size_t)a->B * own * 1024 : 0);
+  // (their rows, then one mark a row)
+  p.total = p.off_rows + (p.rows ? (size_t)a->B * (own * 1024 + align_up((size_t)own, 256)) : 0);
   return p;
 }
 

@@ -24,10 +24,15 @@
 // the probabilities are written with the old one and the CTA's threads agree afterwards, with one barrier, whether that
 // did; a thread sums its own columns until the part ends.
 // A block's last tiles can be the own keys of the sequences it touches (bf16 rows from own_rows_kernel), masked to the rows
-// of their sequence and to what each sees.
+// of their sequence and to what each sees.  An own row that is not finite would reach every row of the block through
+// 0 x NaN: own_rows_kernel writes it as zero and marks it, and the rows that see it get NaN.
 // Parts: the tiles of all blocks of 128 rows form one line that is cut evenly over the pairs, so a pair works on the end
 // of one block and the start of the next, and each leaves a partial (O / l in scaled fp16, lse) that the
 // merge adds.
+// Measured (replayed graphs, 1.85 GHz under the power cap): 64 sequences of 64 heads over 8192 shared entries take about
+// 70 us here, 6700 cycles a tile (128 rows x 256 keys a pair) of which the MMAs need 4096: S 2700 (its operands arrive
+// at the L2's rate), the wake-up of the softmax warps 300, softmax 2000, O 1750.  One pair has no room for a second
+// S (O's accumulator and the operands fill tensor and shared memory), so softmax and MMAs take turns.
 // Every wait is bounded; a wait that gives up records device error 1 and the kernel leaves.
 // Sources: "DeepSeek-V4: エージェントが実際に使える100万トークンのコンテキスト", §ハイブリッド注意, Fig. 4 (the 128x layer
 // attends densely over all visible entries).
@@ -68,6 +73,7 @@ struct PxParams {
   int nseq, otiles;       // own keys: sequences a block can touch, tiles of one sequence (0: attended elsewhere)
   int B, Nq, H, ratio, n_p, n_max;
   int E, Wn, window;      // own rows of a sequence: entries n_p .. n_p + E - 1, then Wn window rows
+  const uint8_t* bad;     // [B][256 otiles] 1: an own row that holds NaN or infinities (and reads as zero)
   int early;              // the kernel before this one is own_rows_kernel: only own tiles wait for it
   const int64_t* win_pos0;
   int slot0, slots;       // partial slots of a query: this kernel's first, and all
@@ -101,6 +107,9 @@ __device__ __forceinline__ PxTile px_tile(const PxParams& P, long long blk, int 
   }
   return t;
 }
+
+// The lowest n bits (n may be anything).
+__device__ __forceinline__ uint32_t px_low(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
 
 __device__ __forceinline__ float px_exp2(float x) {
   float y;
@@ -289,15 +298,29 @@ __global__ void __launch_bounds__(PX_THREADS, 1) __cluster_dims__(2, 1, 1)
         const bool first = t == g;
         const PxTile w = px_tile(P, blk, (int)(t - blk * P.tiles));
         const int k0 = w.key0 + 32 * kq;         // this thread's first key
+        uint32_t see = 0;                        // which of its 32 keys the row sees
+        bool bad = false;                        // one of them has no finite row: the row's result is NaN
+        if (w.b < 0) {
+          see = px_low(nv - k0);
+        } else if (w.b == b) {
+          see = px_low(ve - k0) | (px_low(wh - k0) & ~px_low(wl - k0));
+          if (see) {
+            pdl_wait();
+            const uint4* at = reinterpret_cast<const uint4*>(P.bad + (size_t)b * P.otiles * PX_KEYS + k0);
+            const uint4 x = at[0], y = at[1];
+            if (x.x | x.y | x.z | x.w | y.x | y.y | y.z | y.w) {
+              const uint8_t* s = reinterpret_cast<const uint8_t*>(at);
+              for (int j = 0; j < 32; ++j) bad |= ((see >> j) & 1) && s[j] != 0;
+            }
+          }
+        }
+        const bool all = see == 0xffffffffu;
         ok = ok && mbar_wait(&S.bar_s, f & 1);
         tc_fence_after();
         // The tile is done with the reference as it is; where that turns out too low for some row (every thread of the CTA
         // learns of it at once), or in a part's first tile, once more with moved references.  The columns come 16 at a
         // time and the loops stay rolled: unrolled over all columns the kernel outgrows the instruction caches, and a
         // tile took a tenth longer.
-        const int e0 = w.b < 0 ? nv - k0 : w.b == b ? ve - k0 : 0;      // keys j < e0 and w0 <= j < w1 are seen
-        const int w0 = wl - k0, w1 = w.b >= 0 && w.b == b ? wh - k0 : w0;
-        const bool all = w.b < 0 && e0 >= 32;
         auto scores = [&](int c, float (&z)[16]) -> float {             // columns 16 c ..; returns their maximum
           uint32_t v[16];
           tmem_ld_x16(lane_base + PX_COL_S + 32 * ch + 16 * c, v);
@@ -307,10 +330,8 @@ __global__ void __launch_bounds__(PX_THREADS, 1) __cluster_dims__(2, 1, 1)
           for (int j = 0; j < 16; ++j) z[j] = __uint_as_float(v[j]);
           if (!all) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const int k = 16 * c + j;
-              if (!(k < e0 || (k >= w0 && k < w1))) z[j] = -INFINITY;
-            }
+            for (int j = 0; j < 16; ++j)
+              if (!((see >> (16 * c + j)) & 1)) z[j] = -INFINITY;
           }
 #pragma unroll
           for (int j = 0; j < 16; ++j) top = fmaxf(top, z[j]);
@@ -370,7 +391,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) __cluster_dims__(2, 1, 1)
           }
           if (again || !px_any(top * P.scale_log2 > m + PX_SLACK)) break;
         }
-        l += lt;
+        l += bad ? __int_as_float(0x7fffffff) : lt;
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
@@ -466,8 +487,11 @@ static void px_own(const csa_attn_args* a, int n_p, int* nseq, int* otiles) {
 }
 
 // Whether the prefix kernel takes the own keys too (as bf16 rows written by own_rows_kernel), or the per-query attention
-// does: by their times.  A tile takes a pair 4.0 us, rows are written at about 4 TB/s; the per-query kernels take about
-// 10 us and 6.9 us a tile of 128 keys on an SM (TA_TILE_US).
+// does: by their times.  A tile takes a pair 4.0 us, rows are written at about 4.2 TB/s; the per-query kernels take about
+// 10 us and 7.9 us a wave of tiles of 128 keys.  Measured, here / there: 16 sequences of 64 heads with 64 own entries
+// after 8192 shared ones 32.7 / 44.6 us, 40 of 16 heads with 3000 after 200 96.0 / 111.8; 64 of 64 with 2000 after
+// 1024 112.2 / 107.1, 200 of 4 with 500 after 300 109.4 / 105.2.  Over 24 such shapes the rule's choice costs 1 % on
+// average, 16 % at most (128 of 16 with 500 after 512, 73.3 / 63.2).
 bool attn_prefix_takes_own(const csa_attn_args* a, int n_p) {
   int nseq, otiles;
   px_own(a, n_p, &nseq, &otiles);
@@ -475,9 +499,9 @@ bool attn_prefix_takes_own(const csa_attn_args* a, int n_p) {
   const double own = (double)a->n_max - n_p + (attn_has_window(a) ? a->Wn : 0);
   if (own * a->B > 2147483647.0) return false;
   const double blocks = (double)((long long)(R + PX_ROWS - 1) / PX_ROWS);
-  const double t_here = 4.0 * blocks * nseq * otiles / 74 + a->B * own * 1.4e3 / 4e6;
+  const double t_here = 4.0 * blocks * nseq * otiles / 74 + a->B * own * 1024 / 4.2e6;
   const double waves = (double)(long long)((rows * (double)(long long)((own + 127) / 128) + 147) / 148);
-  return t_here < 10.0 + 6.9 * waves;
+  return t_here < 10.0 + 7.9 * waves;
 }
 
 // The prefix kernel's plan: pairs of CTAs, and partial slots a query needs (at most `most`).
@@ -489,7 +513,8 @@ void attn_prefix_plan(const csa_attn_args* a, int n_p, bool own, int most, int* 
   const long long tiles = ((long long)n_p + PX_KEYS - 1) / PX_KEYS + (long long)nseq * otiles, T = blocks * tiles;
   // Every part costs about as much as 1.2 tiles on top (its first operands from L2, its epilogue).  Cut evenly over all
   // pairs a pair often has two parts; cut at the blocks' ends (a whole number of pairs a block) it has one, of ever so
-  // many more tiles: 16 sequences over 8192 entries, 8 blocks of 34 tiles, 37.0 us with 74 pairs, 33.1 with 72.
+  // many more tiles: 16 sequences of 64 heads over 8192 entries, 8 blocks of 34 tiles, 35.8 us with 74 pairs, 32.8 with
+  // 72; 24 over 4096 36.6 and 28.4; 64 over 1024 38.2 and 31.4.
   long long G = T < 74 ? T : 74;
   if (T > 74 && blocks <= 74) {
     const long long k = 74 / blocks < tiles ? 74 / blocks : tiles;
@@ -537,6 +562,7 @@ csa_status launch_attn_prefix(const csa_attn_args* a, const void* prefix, int n_
   if (own_rows) px_own(a, n_p, &P.nseq, &P.otiles);
   P.tiles = P.ptiles + P.nseq * P.otiles;
   P.early = own_rows != nullptr;
+  P.bad = (const uint8_t*)own_rows + (size_t)a->B * (P.E + P.Wn) * 1024;
   P.B = a->B; P.window = a->window; P.win_pos0 = a->win_pos0;
   P.T = (R + PX_ROWS - 1) / PX_ROWS * P.tiles;
   P.Nq = a->Nq; P.H = a->H; P.ratio = a->ratio; P.n_p = n_p; P.n_max = a->n_max;

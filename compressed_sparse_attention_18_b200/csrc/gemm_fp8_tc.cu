@@ -17,7 +17,7 @@
 // A cluster of ks CTAs can share a tile, each taking a part of K; the partial sums meet in distributed shared
 // memory and are added in rank order (the same result at every run).
 // Bounds, measured on B200 (replayed graphs, SM clock 1.7 GHz under the power cap): 4096 tokens into two weights of
-// 512 x 4096 24.0 us = 1430 TFLOP/s, 8192 x 4096 x 4096 1690 TFLOP/s.  The same pair kernel without reading the
+// 512 x 4096 23.6 us = 1450 TFLOP/s, 8192 x 4096 x 4096 1690 TFLOP/s.  The same pair kernel without reading the
 // accumulators until the end reaches 1630 / 2000, without the loads as well 1970 / 2300: what is left is the
 // hand-over of two accumulators (all of tensor memory) and the operand traffic.  Few tokens are bound by latency:
 // 32 tokens into the two weights take 5.2 us, 4 MB of weights at the copy rate 0.65 us.
@@ -606,6 +606,8 @@ extern "C" csa_status csa_gemm_fp8(const csa_gemm_fp8_args* a, void* stream) {
     while (ks < most && 2 * ks <= KB && tiles * ks * 2 <= 148) ks *= 2;
     return ks == 8 && tiles > 14 ? 4 : ks;
   };
+  // Up to 64 tokens the channels are the MMA's 128 rows.  Measured, two weights of 512 x 4096, channels / tokens there:
+  // 1 token 4.6 / 6.0 us, 32 5.1 / 6.9, 64 6.5 / 7.0, 96 8.2 / 7.3, 128 9.0 / 7.7.
   if (a->M <= 64) {
     const long long tiles = ((long long)a->N + 127) / 128 * nw;
     const int ks = parts(tiles, GF_MAX_CLUSTER);
@@ -613,8 +615,8 @@ extern "C" csa_status csa_gemm_fp8(const csa_gemm_fp8_args* a, void* stream) {
     if (a->M <= 32) return launch_gemm_fp8<32, true>(a, ks, st);
     return launch_gemm_fp8<64, true>(a, ks, st);
   }
-  // Tiles of 128 x 128 while they fill one wave at most, pairs of CTAs on 256 x 256 beyond: 2048 / 4096 tokens into
-  // two weights of 512 x 4096 take 14.2 / 29.4 us with the former and 15.2 (256 x 128) / 24.0 us with the latter.
+  // Tiles of 128 x 128 while they fill one wave at most, pairs of CTAs on 256 x 256 beyond: 2304 / 2560 / 4096 tokens
+  // into two weights of 512 x 4096 take 14.9 / 25.1 / 28.4 us with the former and 20.0 / 20.5 / 23.6 us with the latter.
   const long long tiles128 = ((long long)a->M + 127) / 128 * (((long long)a->N + 127) / 128) * nw;
   if (tiles128 < 148) return launch_gemm_fp8<128, false>(a, parts(tiles128, 4), st);
   return launch_gemm_fp8_pair(a, st);

@@ -99,7 +99,8 @@ __global__ void __launch_bounds__(256) unpack_kernel(const UnpackParams P) {
 }
 
 // A sequence's own keys for the shared-prefix attention, bf16 rows of 512: cache entries first .. n_max - 1 (zero from
-// n_c on: the cache holds anything there), then the window buffer.  One warp per row as above.
+// n_c on: the cache holds anything there), then the window buffer.  A row with a NaN or an infinity becomes zero and is
+// marked, since the attention multiplies rows with weights of queries that do not see them.  One warp per row as above.
 struct OwnRowsParams {
   uint32_t total, per;     // rows, and of one sequence: E entries, then the window's
   int first, E, n_max, Wn;
@@ -113,6 +114,8 @@ struct OwnRowsParams {
   const float* wscales;
   const uint16_t* wrope;
   uint16_t* out;
+  uint8_t* bad;            // [B][stride]: 1 for a row that is not finite
+  uint32_t stride;
   csa_page_map pm;
 };
 
@@ -153,12 +156,22 @@ __global__ void __launch_bounds__(256) own_rows_kernel(const OwnRowsParams P) {
       }
     }
   }
+  bool bad = false;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t x[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bad |= (x[i] & 0x7F800000u) == 0x7F800000u || (x[i] & 0x7F80u) == 0x7F80u;
+  }
+  bad = __any_sync(0xffffffffu, bad);
+  if (bad) v[0] = v[1] = make_uint4(0, 0, 0, 0);
+  if (lane == 0) P.bad[(size_t)b * P.stride + u] = bad;
   uint4* o = reinterpret_cast<uint4*>(P.out + (size_t)r * 512);
   o[lane] = v[0];
   o[lane + 32] = v[1];
 }
 
-// Writes [B][n_max - first + Wn][512]; the caller checked shapes and alignment (d = 512, d_rope = 64).
+// Writes [B][n_max - first + Wn][512] and, behind it, the marks, one byte a row and 256-byte multiples a sequence; the caller checked shapes and alignment (d = 512, d_rope = 64).
 csa_status launch_own_rows(const csa_attn_args* a, int first, void* out, cudaStream_t st) {
   OwnRowsParams P{};
   const bool has_win = attn_has_window(a);
@@ -173,6 +186,7 @@ csa_status launch_own_rows(const csa_attn_args* a, int first, void* out, cudaStr
     P.win = (const uint16_t*)a->win_kv;
   }
   P.out = (uint16_t*)out; P.pm = a->kv_pages;
+  P.bad = (uint8_t*)out + (size_t)total * 1024; P.stride = (uint32_t)((per + 255) / 256 * 256);
   static std::atomic<unsigned> attr_done{0};
   set_smem_once((const void*)own_rows_kernel, 0, attr_done);
   return launch_pdl(own_rows_kernel, dim3((unsigned)((total + 7) / 8)), dim3(256), 0, st, P);

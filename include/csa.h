@@ -453,7 +453,8 @@ csa_status csa_unpack_fp8_window(const csa_unpack_args* args, void* stream);
  *   attn: the arguments of hca_dense_attn.  Entry numbers stay the sequence's own: n_c[b] counts the prefix, entry i
  *         is visible iff i < n_c[b] and ratio*i + ratio - 1 <= t, and rows [0, n_prefix) of the cache are never read
  *         (a paged cache needs no pages for the whole pages among them).  flags must be 0, softmax_scale >= 0.
- * Every row of prefix_kv must hold finite values (rows a query does not see get weight exactly 0).
+ * Every row of prefix_kv must hold finite values (rows a query does not see get weight exactly 0).  An own entry or
+ * window row that holds a NaN or an infinity makes the results of the queries that see it NaN, and of no others.
  * Limits: d = 512, H <= 64, 0 <= n_prefix <= n_max, B * Nq * H < 2^31 - 128; q, prefix_kv, the cache, the window and
  *         the workspace 16-byte aligned (else CSA_ERR_UNSUPPORTED).
  * Workspace: csa_shared_attn_workspace_size() (partials).  Results do not depend on what the workspace held.

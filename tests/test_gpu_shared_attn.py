@@ -149,13 +149,40 @@ def test_same_as_the_unshared_attention(cuda_lib):
 
 
 @pytest.mark.parametrize("B,Nq,H,n_p,own,fp8", [(40, 1, 16, 200, 3000, False), (40, 1, 16, 200, 3000, True),
-                                                (3, 1, 64, 300, 600, False), (130, 1, 1, 300, 9, False), (9, 3, 7, 300, 50, True)])
+                                                (3, 1, 64, 300, 600, False), (130, 1, 1, 300, 9, False), (9, 3, 7, 300, 50, True),
+                                                (130, 1, 1, 300, 500, False), (130, 1, 1, 300, 500, True)])
 def test_own_keys_long_and_many(cuda_lib, B, Nq, H, n_p, own, fp8):
     """Own entries that outnumber the prefix in many sequences (attended query by query), several tiles of them in few
     sequences, and blocks of rows that touch many sequences or cut them at odd places."""
     c = Case(cuda_lib, B, Nq, H, n_p, own, fp8=fp8, seed=B)
     out, lse = c.run(cuda_lib)
     c.check(out, lse, rows=(0, B // 2, B - 1))
+
+
+@pytest.mark.parametrize("fp8,page", [(False, 0), (True, 128)])
+def test_own_rows_that_are_not_finite_stay_with_their_readers(cuda_lib, fp8, page):
+    """Sequences share blocks of query rows: a NaN or infinity in one's cache or window makes NaN of the queries that see
+    it, and changes nothing for the others, bit for bit."""
+    csa = cuda_lib
+    n_p, own, B, Nq = 300, 40, 5, 2
+    n_c = [n_p + own - 1, n_p + 7, n_p, n_p + own, n_p + 1]
+    c = Case(csa, B, Nq, 16, n_p, own, fp8=fp8, page=page, n_c=n_c, t=[[128 * n + 5 + j for j in range(Nq)] for n in n_c],
+             seed=11)
+    out, lse = c.run(csa)
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    win = c.win.rope if fp8 else c.win                      # [B, W + Nq - 1, ..]: query j sees rows j .. j + W - 1
+    win[1, 0, -1] = float("nan")                            # query 0 alone
+    win[2, W, 3] = float("inf")                             # query 1 alone
+    rope = c.cache.rope.view(-1, DR)
+    def row(b, i):
+        return int(c.cache.table[b, i // page]) * page + i % page if page else b * (n_p + own) + i
+    rope[row(3, n_p + own - 1), 0] = float("-inf")          # both of sequence 3
+    rope[row(0, n_p + own - 1), 0] = float("nan")           # entry n_c[0]: nobody
+    o2, l2 = c.run(csa)
+    hit = torch.zeros(B, Nq, dtype=torch.bool, device=DEV)
+    hit[1, 0] = hit[2, 1] = hit[3, 0] = hit[3, 1] = True
+    assert torch.isnan(o2[hit]).all() and torch.isnan(l2[hit]).all()
+    assert torch.equal(o2[~hit], out[~hit]) and torch.equal(l2[~hit], lse[~hit])
 
 
 def test_no_prefix_is_the_plain_attention(cuda_lib):
