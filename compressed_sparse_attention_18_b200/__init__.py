@@ -188,11 +188,23 @@ def _need(t, what, dtype, shape=None, like=None):
     """Check one tensor argument of a call: its type, its shape (None: any size) and that it is on `like`'s device."""
     if not isinstance(t, torch.Tensor) or t.dtype != dtype:
         raise CSAError(f"{what}: a {dtype} tensor is needed")
-    if shape is not None and t.shape != shape:
-        if t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape)):
-            raise CSAError(f"{what}: shape {tuple(t.shape)}, expected {tuple('any' if w is None else w for w in shape)}")
-    if like is not None and t.device != like.device:
+    if shape is not None:
+        have = t.shape
+        ok = len(have) == len(shape)
+        if ok:
+            for w, g in zip(shape, have):
+                if w != g and w is not None:
+                    ok = False
+                    break
+        if not ok:
+            raise CSAError(f"{what}: shape {tuple(have)}, expected {tuple('any' if w is None else w for w in shape)}")
+    if like is not None and t.get_device() != like.get_device():
         raise CSAError(f"{what}: on {t.device}, the other operands are on {like.device}")
+
+
+def _empty(rows, cols, dtype, like):
+    """A contiguous [rows, cols] tensor on `like`'s device (empty_strided: half the host time of new_empty)."""
+    return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=like.device)
 
 
 def _launch(t, stream, call, *args):
@@ -494,14 +506,15 @@ def _shared_args(q, q_pos, cache, n_c, prefix_kv, win_kv, win_pos0, ratio, windo
 def _shared_call(st, q, q_pos, cache, n_c, prefix_kv, win_kv, win_pos0, ratio, window, softmax_scale, out, lse, ws,
                  out_rope_theta):
     if out is None:
-        out = q.new_empty(q.shape)
+        out = torch.empty_like(q)
     if lse is None:
-        lse = q.new_empty(q.shape[:3], dtype=torch.float32)
+        B, Nq, H, _ = q.shape
+        lse = torch.empty_strided((B, Nq, H), (Nq * H, H, 1), dtype=torch.float32, device=q.device)
     a = _shared_args(q, q_pos, cache, n_c, prefix_kv, win_kv, win_pos0, ratio, window, softmax_scale, out, lse,
                      out_rope_theta)
     nbytes = _lib.csa_shared_attn_workspace_size(ctypes.byref(a))
     if nbytes and ws is None:
-        ws = q.new_empty((nbytes,), dtype=torch.uint8)
+        ws = torch.empty_strided((nbytes,), (1,), dtype=torch.uint8, device=q.device)
     have = ws.numel() * ws.element_size() if ws is not None else 0
     _check(_lib.hca_shared_attn(ctypes.byref(a), _ptr(ws), have, st), "hca_shared_attn")
     return out, lse
@@ -566,8 +579,8 @@ class Fp8Blocks:
 def _quant_call(st, src, rows, K, block_rows, out):
     if out is None:
         out = Fp8Blocks.__new__(Fp8Blocks)
-        out.codes = src.new_empty((rows, K), dtype=torch.uint8)
-        out.scales = src.new_empty((-(-rows // block_rows), -(-K // 128)), dtype=torch.float32)
+        out.codes = _empty(rows, K, torch.uint8, src)
+        out.scales = _empty(-(-rows // block_rows), -(-K // 128), torch.float32, src)
         out.block_rows = block_rows
     a = QuantFp8Args(ctypes.sizeof(QuantFp8Args), rows, K, block_rows, _ptr(src), _ptr(out.codes), _ptr(out.scales))
     _check(_lib.csa_quant_fp8(ctypes.byref(a), st), "csa_quant_fp8")
@@ -593,9 +606,9 @@ def _gemm_call(st, x, W, W2, out, out2):
     M, K = x.codes.shape
     N = W.codes.shape[0]
     if out is None:
-        out = x.scales.new_empty((M, N), dtype=torch.bfloat16)
+        out = _empty(M, N, torch.bfloat16, x.scales)
     if W2 is not None and out2 is None:
-        out2 = x.scales.new_empty((M, N), dtype=torch.bfloat16)
+        out2 = _empty(M, N, torch.bfloat16, x.scales)
     a = GemmFp8Args(ctypes.sizeof(GemmFp8Args), M, N, K, _ptr(x.codes), _ptr(x.scales), _ptr(W.codes),
                     _ptr(W2.codes) if W2 is not None else None, _ptr(W.scales),
                     _ptr(W2.scales) if W2 is not None else None, _ptr(out), _ptr(out2))
@@ -649,7 +662,7 @@ def _project_fp8(x, W_kv, W_g, C, Z, stream):
 def _unpack_call(st, fn, what, cache, n, n_max, g, row0, idx, out, pages):
     B, d, d_r = cache.B, cache.d, cache.d_rope
     if out is None:
-        out = cache.rope.new_empty((B, n, d))
+        out = torch.empty_strided((B, n, d), (n * d, d, 1), dtype=torch.bfloat16, device=cache.codes.device)
     a = UnpackArgs(ctypes.sizeof(UnpackArgs), B, n, d, d_r, n_max, g, _ptr(cache.codes), _ptr(cache.scales),
                    _ptr(cache.rope) if d_r else None, _ptr(row0), _ptr(idx), _ptr(out), pages)
     _check(fn(ctypes.byref(a), st), what)
