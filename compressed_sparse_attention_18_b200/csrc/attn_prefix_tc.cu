@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) __cluster_dims__(2, 1, 1)
           for (int s = slot + 1; s < P.slot0 + P.pslots; ++s) P.part_lse[prt + (long long)s * P.H] = -INFINITY;
       }
       // This thread's columns 64 ch .. are the dims 64 blk64 .. of its row: fp16 values times a power of two for the 64
-      // (from their largest), 2^-12 off at most where bf16 would be 2^-9, at no more bytes.
+      // (from their largest), 2^-11 off at most where bf16 would be 2^-8, at no more bytes.
       const int blk64 = 4 * (ch >> 1) + 2 * (quad >> 1) + (ch & 1);
       float big = 0.f;
 #pragma unroll 1
