@@ -461,6 +461,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) __cluster_dims__(2, 1, 1)
         }
       }
       tc_fence_before();
+      px_sync();                                 // the next part's first tile writes red, which is warp 0's stage
       g = e;
     }
     if (!ok && lane == 0) atomicOr(&S.err, 1u);

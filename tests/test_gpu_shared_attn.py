@@ -185,6 +185,19 @@ def test_own_rows_that_are_not_finite_stay_with_their_readers(cuda_lib, fp8, pag
     assert torch.equal(o2[~hit], out[~hit]) and torch.equal(l2[~hit], lse[~hit])
 
 
+def test_parts_that_follow_one_another(cuda_lib):
+    """More blocks of query rows than pairs of CTAs, each of few tiles: a pair stores one block's partial while the next
+    block's scores are there already.  The same result at every run, and the unshared attention's."""
+    csa = cuda_lib
+    B, Nq, H, n_p, own = 130, 3, 34, 257, 900
+    c = Case(csa, B, Nq, H, n_p, own, r=4, seed=59, q_std=4.0)
+    out, lse = c.run(csa)
+    c.check(out, lse, rows=(0, 4, 77, B - 1))
+    for _ in range(5):
+        o2, l2 = c.run(csa)
+        assert torch.equal(o2, out) and torch.equal(l2, lse)
+
+
 def test_no_prefix_is_the_plain_attention(cuda_lib):
     csa = cuda_lib
     c = Case(csa, 3, 1, 16, 0, 200, seed=2)
