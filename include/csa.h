@@ -457,7 +457,7 @@ csa_status csa_unpack_fp8_window(const csa_unpack_args* args, void* stream);
  * window row that holds a NaN or an infinity makes the results of the queries that see it NaN, and of no others.
  * Limits: d = 512, H <= 64, 0 <= n_prefix <= n_max, B * Nq * H < 2^31 - 128; q, prefix_kv, the cache, the window and
  *         the workspace 16-byte aligned (else CSA_ERR_UNSUPPORTED).
- * Workspace: csa_shared_attn_workspace_size() (partials).  Results do not depend on what the workspace held.
+ * Workspace: csa_shared_attn_workspace_size() (partials, and the own keys as bf16 rows).  Results do not depend on what the workspace held.
  * ------------------------------------------------------------------------------------------------ */
 typedef struct csa_shared_attn_args {
   uint32_t struct_size;
