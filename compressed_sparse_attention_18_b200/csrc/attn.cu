@@ -745,7 +745,8 @@ __global__ void __launch_bounds__(SMERGE_WARPS * 32)
   pdl_trigger();
   pdl_wait();
   if (unit >= units) return;                     // (W > 1: every unit has a CTA)
-  const long long bq = unit / H, row0 = bq * slots * H + unit % H;
+  const uint32_t bq = (uint32_t)unit / (uint32_t)H;              // (fewer than 2^31 units)
+  const long long row0 = (long long)bq * slots * H + ((uint32_t)unit - bq * H);
   uint4 v[SMERGE_AT_ONCE][2];
   float ls[SMERGE_AT_ONCE], sc[SMERGE_AT_ONCE];
   auto fetch = [&](int s0) {
@@ -877,6 +878,7 @@ static csa_status run_shared(const csa_shared_attn_args* s, void* ws, size_t ws_
   const long long rows = (long long)a->B * a->Nq;
   if (rows == 0) return CSA_OK;
   const SharedPlan p = plan_shared(s);
+  CSA_SUPPORTED(p.pairs > 0);
   if (ws_bytes < p.total) return CSA_ERR_WORKSPACE;
   CSA_REQUIRE(ws != nullptr);
   CSA_SUPPORTED(((uintptr_t)ws & 15) == 0);
@@ -901,7 +903,9 @@ using namespace csa;
 
 extern "C" size_t csa_shared_attn_workspace_size(const csa_shared_attn_args* a) {
   if (validate_shared(a, false) != CSA_OK || (long long)a->attn.B * a->attn.Nq == 0) return 0;
-  return a->n_prefix == 0 ? plan_attn(&a->attn, 1).total : plan_shared(a).total;
+  if (a->n_prefix == 0) return plan_attn(&a->attn, 1).total;
+  const SharedPlan p = plan_shared(a);
+  return p.pairs > 0 ? p.total : 0;
 }
 
 extern "C" csa_status hca_shared_attn(const csa_shared_attn_args* a, void* ws, size_t ws_bytes, void* stream) {

@@ -67,7 +67,8 @@ struct PxSmem {
 
 struct PxParams {
   long long R;            // query rows: B * Nq * H
-  long long T;            // tiles of all blocks
+  long long T;            // tiles of all blocks (< 2^31), its quotient and remainder by the pairs
+  int T_quot, T_rem;
   int tiles;              // tiles of one block: of the prefix, then nseq * otiles of own keys
   int ptiles;             // tiles of the prefix: ceil(n_p / 256)
   int nseq, otiles;       // own keys: sequences a block can touch, tiles of one sequence (0: attended elsewhere)
@@ -100,7 +101,7 @@ __device__ __forceinline__ PxTile px_tile(const PxParams& P, long long blk, int 
     t.key0 = t.row0 = i * PX_KEYS;
   } else {
     const int o = i - P.ptiles, s = o / P.otiles;
-    t.b = (int)(blk * PX_ROWS / ((long long)P.Nq * P.H)) + s;
+    t.b = (int)((uint32_t)(blk * PX_ROWS) / (uint32_t)(P.Nq * P.H)) + s;
     t.key0 = (o - s * P.otiles) * PX_KEYS;
     // (a sequence behind the last: some rows that no query row is matched with)
     t.row0 = min(t.b, P.B - 1) * (P.E + P.Wn) + t.key0;
@@ -134,7 +135,9 @@ __global__ void __launch_bounds__(PX_THREADS, 1) __cluster_dims__(2, 1, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = (int)blockIdx.x & 1;
   const long long pair = blockIdx.x >> 1, G = gridDim.x >> 1;
-  const long long g_begin = pair * P.T / G, g_end = (pair + 1) * P.T / G;
+  // floor(pair T / G) and the next pair's, from T's quotient and remainder by G
+  auto cut = [&](int i) { return i * P.T_quot + (int)((uint32_t)(i * P.T_rem) / (uint32_t)G); };
+  const long long g_begin = cut((int)pair), g_end = cut((int)pair + 1);
   if (tid == 0) {
     S.err = 0;
     for (int i = 0; i < 8; ++i) { mbar_init(&S.full[i], 1); mbar_init(&S.rel[i], 1); mbar_init(&S.bar_q[i], 1); }
@@ -162,7 +165,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) __cluster_dims__(2, 1, 1)
     if (lane == 0) {
       uint32_t tile = 0, part = 0;
       for (long long g = g_begin; g < g_end && ok; ++part) {
-        const long long blk = g / P.tiles, blk_end = (blk + 1) * P.tiles, e = blk_end < g_end ? blk_end : g_end;
+        const long long blk = (uint32_t)g / (uint32_t)P.tiles, blk_end = (blk + 1) * P.tiles, e = blk_end < g_end ? blk_end : g_end;
         // the previous part's S MMAs have read Q
         if (part > 0 && !mbar_wait(&S.bar_qfree, (part - 1) & 1)) { ok = false; break; }
         bool q_due = true;                       // Q's dim blocks go with the first tile's chunks
@@ -210,7 +213,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) __cluster_dims__(2, 1, 1)
       };
       uint32_t f = 0, part = 0;
       for (long long g = g_begin; g < g_end && ok; ++part) {
-        const long long blk_end = (g / P.tiles + 1) * P.tiles, e = blk_end < g_end ? blk_end : g_end;
+        const long long blk_end = ((uint32_t)g / (uint32_t)P.tiles + 1LL) * P.tiles, e = blk_end < g_end ? blk_end : g_end;
         const int n = (int)(e - g);
 #pragma unroll 1
         for (int t = 0; t < n && ok; ++t, ++f) {
@@ -272,7 +275,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) __cluster_dims__(2, 1, 1)
     const uint32_t bar_p = peer_addr(&S.bar_p, 0);
     uint32_t f = 0, part = 0;
     for (long long g = g_begin; g < g_end; ++part) {
-      const long long blk = g / P.tiles, blk_end = (blk + 1) * P.tiles, e = blk_end < g_end ? blk_end : g_end;
+      const long long blk = (uint32_t)g / (uint32_t)P.tiles, blk_end = (blk + 1) * P.tiles, e = blk_end < g_end ? blk_end : g_end;
       // how many entries the row sees (rows behind the last query row: all of them, their Q is zero and nothing is
       // stored), and its place in the partials without the slot
       const long long qr = blk * PX_ROWS + 64 * rank + row;
@@ -281,8 +284,8 @@ __global__ void __launch_bounds__(PX_THREADS, 1) __cluster_dims__(2, 1, 1)
       int nv = P.n_p, b = -2, ve = 0, wl = 0, wh = 0;
       long long prt = 0;
       if (real) {
-        const long long bq = qr / P.H, tq = P.q_pos[bq];
-        b = (int)(bq / P.Nq);
+        const long long bq = (uint32_t)qr / (uint32_t)P.H, tq = P.q_pos[bq];
+        b = (int)bq / P.Nq;
         const int see = (int)max(0LL, min((long long)min(P.n_c[b], P.n_max), (tq + 1) / P.ratio));
         nv = min(P.n_p, see);
         ve = max(0, see - P.n_p);
@@ -505,13 +508,15 @@ bool attn_prefix_takes_own(const csa_attn_args* a, int n_p) {
   return t_here < 10.0 + 7.9 * waves;
 }
 
-// The prefix kernel's plan: pairs of CTAs, and partial slots a query needs (at most `most`).
+// The prefix kernel's plan: pairs of CTAs, and partial slots a query needs (at most `most`); 0 pairs: too many tiles.
 void attn_prefix_plan(const csa_attn_args* a, int n_p, bool own, int most, int* pairs, int* slots) {
   const long long R = (long long)a->B * a->Nq * a->H;
   int nseq = 0, otiles = 0;
   if (own) px_own(a, n_p, &nseq, &otiles);
   const long long blocks = (R + PX_ROWS - 1) / PX_ROWS;
   const long long tiles = ((long long)n_p + PX_KEYS - 1) / PX_KEYS + (long long)nseq * otiles, T = blocks * tiles;
+  *pairs = *slots = 0;
+  if (T > 0x7fffffffLL) return;                            // (the kernel counts tiles in 32 bits)
   // Every part costs about as much as 1.2 tiles on top (its first operands from L2, its epilogue).  Cut evenly over all
   // pairs a pair often has two parts; cut at the blocks' ends (a whole number of pairs a block) it has one, of ever so
   // many more tiles: 16 sequences of 64 heads over 8192 entries, 8 blocks of 34 tiles, 35.8 us with 74 pairs, 32.8 with
@@ -566,6 +571,7 @@ csa_status launch_attn_prefix(const csa_attn_args* a, const void* prefix, int n_
   P.bad = (const uint8_t*)own_rows + (size_t)a->B * (P.E + P.Wn) * 1024;
   P.B = a->B; P.window = a->window; P.win_pos0 = a->win_pos0;
   P.T = (R + PX_ROWS - 1) / PX_ROWS * P.tiles;
+  P.T_quot = (int)(P.T / pairs); P.T_rem = (int)(P.T % pairs);
   P.Nq = a->Nq; P.H = a->H; P.ratio = a->ratio; P.n_p = n_p; P.n_max = a->n_max;
   P.slot0 = slot0; P.slots = slots; P.pslots = pslots;
   P.scale_log2 = (a->softmax_scale != 0.0f ? a->softmax_scale : 1.0f / sqrtf(512.0f)) * PX_LOG2E;

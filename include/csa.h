@@ -455,9 +455,11 @@ csa_status csa_unpack_fp8_window(const csa_unpack_args* args, void* stream);
  *         (a paged cache needs no pages for the whole pages among them).  flags must be 0, softmax_scale >= 0.
  * Every row of prefix_kv must hold finite values (rows a query does not see get weight exactly 0).  An own entry or
  * window row that holds a NaN or an infinity makes the results of the queries that see it NaN, and of no others.
- * Limits: d = 512, H <= 64, 0 <= n_prefix <= n_max, B * Nq * H < 2^31 - 128; q, prefix_kv, the cache, the window and
- *         the workspace 16-byte aligned (else CSA_ERR_UNSUPPORTED).
- * Workspace: csa_shared_attn_workspace_size() (partials, and the own keys as bf16 rows).  Results do not depend on what the workspace held.
+ * Limits: d = 512, H <= 64, 0 <= n_prefix <= n_max, B * Nq * H < 2^31 - 128, fewer than 2^31 tiles of
+ *         128 query rows x 256 keys; q, prefix_kv, the cache, the window and the workspace 16-byte aligned (else
+ *         CSA_ERR_UNSUPPORTED).
+ * Workspace: csa_shared_attn_workspace_size() (partials, and the own keys as bf16 rows).  Results do not depend on what
+ * the workspace held.
  * ------------------------------------------------------------------------------------------------ */
 typedef struct csa_shared_attn_args {
   uint32_t struct_size;

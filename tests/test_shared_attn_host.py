@@ -56,6 +56,7 @@ def test_refusals(csa):
     assert call(csa, flags=1) == UNSUPPORTED and call(csa, flags=2) == UNSUPPORTED
     assert call(csa, prefix=ODD) == UNSUPPORTED and call(csa, q=ODD) == UNSUPPORTED and call(csa, kv_codes=ODD) == UNSUPPORTED
     assert call(csa, B=1 << 20, Nq=64, H=64) == UNSUPPORTED           # 2^32 query rows
+    assert call(csa, B=1, Nq=1 << 20, H=64, n_prefix=1 << 21, n_max=1 << 21) == UNSUPPORTED
     assert call(csa) in (WORKSPACE, UNSUPPORTED)                       # (no tensor maps without a driver)
     assert call(csa, B=0) == OK
 
@@ -71,6 +72,8 @@ def test_workspace_sizes(csa):
     assert size(n_prefix=700, n_max=800) >= 4 * row
     # a long prefix is cut into at most 128 parts
     assert size(n_prefix=1 << 20, n_max=1 << 20) <= 129 * row
+    # 2^32 tiles of 128 query rows x 256 keys
+    assert size(B=1, Nq=1 << 20, H=64, n_prefix=1 << 21, n_max=1 << 21) == 0
     # without a prefix the call is hca_dense_attn
     a = args(csa, n_prefix=0)
     assert size(n_prefix=0) == csa._lib.csa_attn_workspace_size(ctypes.byref(a.attn), 1)
