@@ -275,7 +275,8 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1) attn_kernel(AttnParams P) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int h = e >> 1;
-        const float p = (m_r[h] == -INFINITY) ? 0.f : exp2f(sacc[j][e] - m_r[h]);
+        // (no score above -inf yet: masked keys get 0, a NaN stays one and makes l NaN)
+        const float p = exp2f(sacc[j][e] - (m_r[h] == -INFINITY ? 0.f : m_r[h]));
         sacc[j][e] = p;
         rs[h] += p;
       }
@@ -316,8 +317,8 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1) attn_kernel(AttnParams P) {
   float inv_l[2], lse_r[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    inv_l[h] = l_r[h] > 0.f ? 1.f / l_r[h] : 0.f;
-    lse_r[h] = l_r[h] > 0.f ? (m_r[h] + log2f(l_r[h])) * LN2 : -INFINITY;
+    inv_l[h] = l_r[h] == 0.f ? 0.f : 1.f / l_r[h];
+    lse_r[h] = l_r[h] == 0.f ? -INFINITY : (m_r[h] + log2f(l_r[h])) * LN2;
   }
   const int rows[2] = {hg * 16 + g, hg * 16 + g + 8};
   if (P.splits == 1) {
@@ -455,7 +456,7 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) attn_merge_kernel(const PT* 
   for (int i = 0; i < DPL; ++i) acc[i] = 0.f;
   const PT* base = part_o + (bq * splits * H + h) * (long long)D + lane * DPL;
   const float* lrow = part_lse + bq * splits * H + h;
-  float mx = -INFINITY, sum = 0.f;
+  float mx = -INFINITY, sum = 0.f;               // (a NaN lse is not in the max, but its weight makes the row NaN)
   if (splits <= MERGE_CHUNK) {
     // one round: every lane loads all split lse values (broadcast) and its dims of every partial; empty
     // splits (lse = -inf, partial never written) are dropped by a select, never multiplied
@@ -470,7 +471,7 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) attn_merge_kernel(const PT* 
     for (int c = 0; c < MERGE_CHUNK; ++c) mx = fmaxf(mx, ls[c]);
 #pragma unroll
     for (int c = 0; c < MERGE_CHUNK; ++c) {
-      const float w = (mx == -INFINITY || ls[c] == -INFINITY) ? 0.f : exp2f((ls[c] - mx) * LOG2E);
+      const float w = ls[c] == -INFINITY ? 0.f : exp2f((ls[c] - mx) * LOG2E);
       sum += w;
       if (w != 0.f)
 #pragma unroll
@@ -482,7 +483,7 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) attn_merge_kernel(const PT* 
     mx = warp_max(mx);
     for (int s = lane; s < splits; s += 32) {
       const float l = lrow[(long long)s * H];
-      sum += (mx == -INFINITY || l == -INFINITY) ? 0.f : exp2f((l - mx) * LOG2E);
+      sum += l == -INFINITY ? 0.f : exp2f((l - mx) * LOG2E);
     }
     sum = warp_sum(sum);
     for (int s0 = 0; s0 < splits; s0 += MERGE_CHUNK) {
@@ -494,7 +495,7 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) attn_merge_kernel(const PT* 
         wgt[c] = 0.f;
         if (s < splits) {
           const float l = lrow[(long long)s * H];
-          wgt[c] = (mx == -INFINITY || l == -INFINITY) ? 0.f : exp2f((l - mx) * LOG2E);
+          wgt[c] = l == -INFINITY ? 0.f : exp2f((l - mx) * LOG2E);
         }
         if (wgt[c] != 0.f) v[c].load(base + (long long)s * H * D);
       }
@@ -505,7 +506,7 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) attn_merge_kernel(const PT* 
           for (int i = 0; i < DPL; ++i) acc[i] = fmaf(wgt[c], v[c].get(i), acc[i]);
     }
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
   for (int i = 0; i < DPL; ++i) acc[i] *= inv;
   if (rope_theta != 0.f) inverse_rope_lanes<D>(acc, lane, q_pos[bq], rope_theta);
@@ -519,7 +520,7 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) attn_merge_kernel(const PT* 
   } else {
     *reinterpret_cast<uint2*>(o) = make_uint2(pk[0], pk[1]);
   }
-  if (lse && lane == 0) lse[bq * H + h] = sum > 0.f ? mx + logf(sum) : -INFINITY;
+  if (lse && lane == 0) lse[bq * H + h] = sum == 0.f ? -INFINITY : mx + logf(sum);
   pdl_trigger();
 }
 

@@ -43,7 +43,11 @@ struct TaSmem {
   alignas(1024) uint8_t Q[8][64 * 128];        // [dim block][head][128 B]
   alignas(1024) uint8_t P[TA_KEYS * 128];      // [key][64 heads bf16]
   float red_m[4][64], red_l[4][64];            // per lane-quadrant partial max / sum
-  alignas(16) float m[64];                     // running max (log2 units)
+  // What a head's probabilities are taken against: its running max, 0 while no key has had a score above -inf, so that
+  // masked keys get 0 and a NaN stays one.  A NaN score has no part in the max, but its probability makes the head's sum,
+  // lse and outputs NaN; only a sum of exactly 0 means "no keys" (here and in the merges).
+  alignas(16) float ref[64];
+  float m[64];                                 // running max (log2 units)
   float l[64], fac[64];                        // running sum, this tile's rescale
   int32_t ids[TA_KEYS];                        // entry id of each entry row, -1 if absent
   // per dim block: Q landed, window boxes landed, gathered rows written
@@ -561,6 +565,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
           f = mo == -INFINITY ? 0.f : exp2f(mo - mn);
         }
         S.m[tid] = mn;
+        S.ref[tid] = mn == -INFINITY ? 0.f : mn;
         S.fac[tid] = f;
         S.l[tid] *= f;
         if (f != 1.f && t > 0) S.rescale = 1;
@@ -587,16 +592,15 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
         float mh[32];
 #pragma unroll
         for (int j = 0; j < 32; j += 4) {
-          const float4 v4 = *reinterpret_cast<const float4*>(&S.m[hh * 32 + j]);
+          const float4 v4 = *reinterpret_cast<const float4*>(&S.ref[hh * 32 + j]);
           mh[j] = v4.x; mh[j + 1] = v4.y; mh[j + 2] = v4.z; mh[j + 3] = v4.w;
         }
 #pragma unroll
         for (int j = 0; j < 32; j += 2) {
-          const float m0 = mh[j], m1 = mh[j + 1];
           const float z0 = valid ? __uint_as_float(sv[j]) * P.scale_log2 : -INFINITY;
           const float z1 = valid ? __uint_as_float(sv[j + 1]) * P.scale_log2 : -INFINITY;
-          const float p0f = m0 == -INFINITY ? 0.f : ta_exp2(z0 - m0);
-          const float p1f = m1 == -INFINITY ? 0.f : ta_exp2(z1 - m1);
+          const float p0f = ta_exp2(z0 - mh[j]);
+          const float p1f = ta_exp2(z1 - mh[j + 1]);
           red[j] = p0f;
           red[j + 1] = p1f;
           pk[j >> 1] = pack_bf16x2(p0f, p1f);
@@ -628,7 +632,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
       const float lj = S.l[hh * 32 + j];
-      il[j] = lj > 0.f ? 1.f / lj : 0.f;
+      il[j] = lj == 0.f ? 0.f : 1.f / lj;
     }
     const int hmax = min(32, P.H - hh * 32);
     const int tl = ntile - 1;
@@ -666,7 +670,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
     if (!ok && lane == 0) atomicOr(&S.err, 1u);
     if (tid < P.H && !P.cluster) {
       const float lh = S.l[tid];
-      const float ls = lh > 0.f ? (S.m[tid] + log2f(lh)) * TA_LN2 : -INFINITY;
+      const float ls = lh == 0.f ? -INFINITY : (S.m[tid] + log2f(lh)) * TA_LN2;
       if (P.part_o == nullptr) {
         if (P.lse) P.lse[(size_t)bq * P.H + tid] = ls;
       } else {
@@ -690,18 +694,18 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
         if (r < ns) {
           mr[r] = ld_peer_f32(peer_addr(&S.m[tid], r));
           lr[r] = ld_peer_f32(peer_addr(&S.l[tid], r));
-          if (lr[r] > 0.f) M = fmaxf(M, mr[r]);
+          if (lr[r] != 0.f) M = fmaxf(M, mr[r]);
         }
       }
       float L = 0.f;
 #pragma unroll
       for (int r = 0; r < TA_MAX_CLUSTER; ++r) {
-        const float f = (r < ns && lr[r] > 0.f) ? exp2f(mr[r] - M) : 0.f;
+        const float f = (r < ns && lr[r] != 0.f) ? exp2f(mr[r] - M) : 0.f;
         S.cf[r][tid] = f;
         L += f * lr[r];
       }
-      S.cL[tid] = L > 0.f ? 1.f / L : 0.f;
-      if (split == 0 && P.lse && tid < P.H) P.lse[(size_t)bq * P.H + tid] = L > 0.f ? (M + log2f(L)) * TA_LN2 : -INFINITY;
+      S.cL[tid] = L == 0.f ? 0.f : 1.f / L;
+      if (split == 0 && P.lse && tid < P.H) P.lse[(size_t)bq * P.H + tid] = L == 0.f ? -INFINITY : (M + log2f(L)) * TA_LN2;
     }
     __syncthreads();
     const int per = ((512 + ns - 1) / ns + 3) & ~3;
@@ -855,8 +859,8 @@ __device__ __forceinline__ bool ta_epilogue(TaSmem& S, const TaParams& P, int ui
   float* lrow = part ? P.part_lse + ta_part(P, uid) * P.H : (P.lse ? P.lse + (size_t)uid * P.H : nullptr);
   if (tid < 64) {
     const float lh = S.l[tid];
-    S.fac[tid] = lh > 0.f ? 1.f / lh : 0.f;
-    if (tid < P.H && lrow) lrow[tid] = lh > 0.f ? (S.m[tid] + log2f(lh)) * TA_LN2 : -INFINITY;
+    S.fac[tid] = lh == 0.f ? 0.f : 1.f / lh;
+    if (tid < P.H && lrow) lrow[tid] = lh == 0.f ? -INFINITY : (S.m[tid] + log2f(lh)) * TA_LN2;
     S.m[tid] = -INFINITY;
     S.l[tid] = 0.f;
   }
@@ -1184,6 +1188,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
           fc = mo == -INFINITY ? 0.f : exp2f(mo - mn);
         }
         S.m[tid] = mn;
+        S.ref[tid] = mn == -INFINITY ? 0.f : mn;
         S.fac[tid] = fc;
         S.l[tid] *= fc;
         if (fc != 1.f && t_cur > 0) S.rescale = 1;
@@ -1209,16 +1214,15 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
         float mh[32];
 #pragma unroll
         for (int j = 0; j < 32; j += 4) {
-          const float4 v4 = *reinterpret_cast<const float4*>(&S.m[hh * 32 + j]);
+          const float4 v4 = *reinterpret_cast<const float4*>(&S.ref[hh * 32 + j]);
           mh[j] = v4.x; mh[j + 1] = v4.y; mh[j + 2] = v4.z; mh[j + 3] = v4.w;
         }
 #pragma unroll
         for (int j = 0; j < 32; j += 2) {
-          const float m0 = mh[j], m1 = mh[j + 1];
           const float z0 = valid ? __uint_as_float(sv[j]) * P.scale_log2 : -INFINITY;
           const float z1 = valid ? __uint_as_float(sv[j + 1]) * P.scale_log2 : -INFINITY;
-          const float p0f = m0 == -INFINITY ? 0.f : ta_exp2(z0 - m0);
-          const float p1f = m1 == -INFINITY ? 0.f : ta_exp2(z1 - m1);
+          const float p0f = ta_exp2(z0 - mh[j]);
+          const float p1f = ta_exp2(z1 - mh[j + 1]);
           red[j] = p0f;
           red[j + 1] = p1f;
           pk[j >> 1] = pack_bf16x2(p0f, p1f);
