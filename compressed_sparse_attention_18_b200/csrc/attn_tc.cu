@@ -186,6 +186,25 @@ __device__ __forceinline__ TaTile ta_tile(int key0, int n_sel, int n_list, long 
   return g;
 }
 
+// True for a score that is NaN or infinite.  A row with such a value has such scores in every column, the heads behind the
+// last included (their queries are zero, and 0 x inf is NaN): one column tells whether to look closer.
+__device__ __forceinline__ bool ta_odd(uint32_t score) { return (score & 0x7F800000u) == 0x7F800000u; }
+
+// The last TMA box of a tile's window rows may bring rows [rw, zs) that the query does not see.  Their scores are masked,
+// but in O they would count 0 x row, which is NaN where the row is not finite: a row of them with an odd score is zeroed
+// by its two threads (head half hh: dim blocks 4 hh ..) after the S MMAs have read the tile and before P is handed over.
+// (Zeroing them whatever they hold took 3 % of an attention over few entries.)  `ph` is the tile's phase of bar_w.
+__device__ __forceinline__ bool ta_zero_row(TaSmem& S, int row, int hh, uint32_t ph) {
+  bool ok = true;
+#pragma unroll 1
+  for (int j = 4 * hh; j < 4 * hh + 4; ++j) {
+    ok = mbar_wait(&S.bar_w[j], ph) && ok;             // (landed: S has read it)
+#pragma unroll 1
+    for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(&S.K[j][row * 128 + c * 16]) = make_uint4(0, 0, 0, 0);
+  }
+  return ok;
+}
+
 // Lazy rescaling: a head keeps its running max until a tile's max exceeds it by more than this (log2
 // units), so probabilities stay <= 2^8 and O is rescaled in tensor memory only when a max jumps.
 constexpr float TA_RESCALE_SLACK = 8.0f;
@@ -551,6 +570,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
         uint32_t sv[32];
         tmem_ld_x32(lane_base + TA_COL_S + hh * 32, sv);
         tmem_wait_ld_x32(sv);
+        if (!W8 && ta_odd(sv[0]) && key >= gt.rw && key < gt.zs) ok = ta_zero_row(S, key, hh, t & 1) && ok;
 #pragma unroll
         for (int j = 0; j < 32; ++j) red[j] = valid ? __uint_as_float(sv[j]) * P.scale_log2 : -INFINITY;
       }
@@ -1152,7 +1172,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
         load_row(un.b, id);
       }
       // what the softmax needs of this tile; then the cursor moves on (one query's geometry stays live)
-      const int rs_t = g.rs, rw_t = g.rw, t_cur = t;
+      const int rs_t = g.rs, rw_t = g.rw, zs_t = g.zs, t_cur = t;
       const int bq_ends = t + 1 == u.ntile ? u.uid : -1;
       k = kn;
       t = tn;
@@ -1174,6 +1194,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
         uint32_t sv[32];
         tmem_ld_x32(lane_base + TA_COL_S + hh * 32, sv);
         tmem_wait_ld_x32(sv);
+        if (ta_odd(sv[0]) && key >= rw_t && key < zs_t) ok = ta_zero_row(S, key, hh, f & 1) && ok;
 #pragma unroll
         for (int j = 0; j < 32; ++j) red[j] = valid ? __uint_as_float(sv[j]) * P.scale_log2 : -INFINITY;
       }

@@ -120,3 +120,35 @@ def test_small_head_attention_with_a_nan(cuda_lib, Nq, n):
     kv.rope[2, 0] = NAN
     kv.rope[2, 1] = NAN                                     # behind n_c
     check_hits(run(), want, torch.tensor([True, False, True], device=DEV)[:, None].expand(B, Nq))
+
+
+@pytest.mark.parametrize("B,Nq,H,n_p,own,fp8", SHAPES + [(3, 5, 8, 0, 333, False), (60, 3, 8, 0, 333, False)])
+def test_window_rows_that_a_query_does_not_see(cuda_lib, B, Nq, H, n_p, own, fp8):
+    """A window buffer longer than the window, NaN in all its rows that nobody sees; then also in the rows of a sequence's
+    later queries, which reach those alone."""
+    csa = cuda_lib
+    c = Case(csa, B, Nq, H, n_p, own, fp8=fp8, n_c=lengths(B, n_p, own), t=positions(B, Nq, n_p, own),
+             seed=B + H + 1)
+    before, behind = 17, 41                                 # rows that end the window inside a block of 32 at many places
+    rows = W + Nq - 1
+    if fp8:
+        wide = csa.Fp8Window(B, before + rows + behind, D, DR, DEV)
+        for name in ("codes", "scales", "rope"):
+            getattr(wide, name)[:, before:before + rows] = getattr(c.win, name)
+        wide.rope[:, :before] = wide.rope[:, before + rows:] = 1.0
+        edge = wide.rope
+    else:
+        wide = edge = torch.ones((B, before + rows + behind, D), dtype=torch.bfloat16, device=DEV)
+        wide[:, before:before + rows] = c.win
+    c.win = wide
+    c.args = c.args[:5] + (wide, c.args[6] - before)
+    want = c.run(csa)
+    edge[:, :before] = NAN
+    edge[:, before + rows:] = NAN
+    hit = torch.zeros(B, Nq, dtype=torch.bool, device=DEV)
+    check_hits(c.run(csa), want, hit)
+    if Nq > 1:
+        for b in range(0, B, 2):
+            edge[b, before + W, 3 + b % 7] = NAN            # the row of the second query: all but the first see it
+            hit[b, 1:] = True
+        check_hits(c.run(csa), want, hit)
