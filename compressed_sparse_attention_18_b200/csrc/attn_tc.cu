@@ -190,6 +190,15 @@ __device__ __forceinline__ TaTile ta_tile(int key0, int n_sel, int n_list, long 
 // last included (their queries are zero, and 0 x inf is NaN): one column tells whether to look closer.
 __device__ __forceinline__ bool ta_odd(uint32_t score) { return (score & 0x7F800000u) == 0x7F800000u; }
 
+// What a key's scores are scaled by: NaN for a row that is not finite (every score odd), so that its readers get NaN
+// whichever infinity their scores are; a score of -inf would be weight 0.
+__device__ __forceinline__ float ta_key_scale(const uint32_t (&sv)[32], float scale) {
+  float low = INFINITY;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) low = fminf(low, fabsf(__uint_as_float(sv[j])));     // (the least that is not NaN)
+  return low < INFINITY ? scale : __int_as_float(0x7FFFFFFF);
+}
+
 // The last TMA box of a tile's window rows may bring rows [rw, zs) that the query does not see.  Their scores are masked,
 // but in O they would count 0 x row, which is NaN where the row is not finite: a row of them with an odd score is zeroed
 // by its two threads (head half hh: dim blocks 4 hh ..) after the S MMAs have read the tile and before P is handed over.
@@ -565,14 +574,17 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
       // one 32-value array per thread: the scores for the max, reloaded from tensor memory for the
       // probabilities, which then feed the sum
       const bool valid = key < gt.rs ? (S.ids[key] >= 0) : (key < gt.rw);
-      float red[32];
+      float red[32], key_scale = P.scale_log2;
       {
         uint32_t sv[32];
         tmem_ld_x32(lane_base + TA_COL_S + hh * 32, sv);
         tmem_wait_ld_x32(sv);
-        if (!W8 && ta_odd(sv[0]) && key >= gt.rw && key < gt.zs) ok = ta_zero_row(S, key, hh, t & 1) && ok;
+        if (ta_odd(sv[0])) {
+          if (valid) key_scale = ta_key_scale(sv, P.scale_log2);
+          else if (!W8 && key >= gt.rw && key < gt.zs) ok = ta_zero_row(S, key, hh, t & 1) && ok;
+        }
 #pragma unroll
-        for (int j = 0; j < 32; ++j) red[j] = valid ? __uint_as_float(sv[j]) * P.scale_log2 : -INFINITY;
+        for (int j = 0; j < 32; ++j) red[j] = valid ? __uint_as_float(sv[j]) * key_scale : -INFINITY;
       }
       S.red_m[quad][hh * 32 + lane] = transpose_reduce32<true>(red, lane);
       asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -617,8 +629,8 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
         }
 #pragma unroll
         for (int j = 0; j < 32; j += 2) {
-          const float z0 = valid ? __uint_as_float(sv[j]) * P.scale_log2 : -INFINITY;
-          const float z1 = valid ? __uint_as_float(sv[j + 1]) * P.scale_log2 : -INFINITY;
+          const float z0 = valid ? __uint_as_float(sv[j]) * key_scale : -INFINITY;
+          const float z1 = valid ? __uint_as_float(sv[j + 1]) * key_scale : -INFINITY;
           const float p0f = ta_exp2(z0 - mh[j]);
           const float p1f = ta_exp2(z1 - mh[j + 1]);
           red[j] = p0f;
@@ -1189,14 +1201,17 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
       ok = ok && mbar_wait(&S.bar_s, f & 1);
       tc_fence_after();
       const bool valid = key < rs_t ? (S.ids[key] >= 0) : (key < rw_t);
-      float red[32];
+      float red[32], key_scale = P.scale_log2;
       {
         uint32_t sv[32];
         tmem_ld_x32(lane_base + TA_COL_S + hh * 32, sv);
         tmem_wait_ld_x32(sv);
-        if (ta_odd(sv[0]) && key >= rw_t && key < zs_t) ok = ta_zero_row(S, key, hh, f & 1) && ok;
+        if (ta_odd(sv[0])) {
+          if (valid) key_scale = ta_key_scale(sv, P.scale_log2);
+          else if (key >= rw_t && key < zs_t) ok = ta_zero_row(S, key, hh, f & 1) && ok;
+        }
 #pragma unroll
-        for (int j = 0; j < 32; ++j) red[j] = valid ? __uint_as_float(sv[j]) * P.scale_log2 : -INFINITY;
+        for (int j = 0; j < 32; ++j) red[j] = valid ? __uint_as_float(sv[j]) * key_scale : -INFINITY;
       }
       S.red_m[quad][hh * 32 + lane] = transpose_reduce32<true>(red, lane);
       asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -1240,8 +1255,8 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
         }
 #pragma unroll
         for (int j = 0; j < 32; j += 2) {
-          const float z0 = valid ? __uint_as_float(sv[j]) * P.scale_log2 : -INFINITY;
-          const float z1 = valid ? __uint_as_float(sv[j + 1]) * P.scale_log2 : -INFINITY;
+          const float z0 = valid ? __uint_as_float(sv[j]) * key_scale : -INFINITY;
+          const float z1 = valid ? __uint_as_float(sv[j + 1]) * key_scale : -INFINITY;
           const float p0f = ta_exp2(z0 - mh[j]);
           const float p1f = ta_exp2(z1 - mh[j + 1]);
           red[j] = p0f;

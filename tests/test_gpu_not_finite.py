@@ -1,6 +1,6 @@
-"""Keys that are not finite: a NaN in an entry or window row makes NaN of every result of the queries that see it, and
-changes nothing for the others, bit for bit, on each route of the attention: the shared-prefix call with the sequences'
-own keys in the per-query and in the persistent kernel and without a prefix, and the plain attentions."""
+"""Keys that are not finite: a NaN or an infinity in an entry or window row makes NaN of every result of the queries that
+see it, and changes nothing for the others, bit for bit, on each route of the attention: the shared-prefix call with the
+sequences' own keys in the per-query and in the persistent kernel and without a prefix, and the plain attentions."""
 import pytest
 import torch
 
@@ -9,7 +9,7 @@ from tests.test_gpu_shared_attn import D, DEV, DR, W, Case
 
 pytestmark = pytest.mark.gpu
 
-NAN = float("nan")
+NAN, INF = float("nan"), float("inf")
 
 # own keys in the per-query kernel (bf16 and FP8 windows), in the persistent kernel (more than 148 queries, bf16 window);
 # without a prefix: several splits merged, whole queries, persistent
@@ -152,3 +152,20 @@ def test_window_rows_that_a_query_does_not_see(cuda_lib, B, Nq, H, n_p, own, fp8
             edge[b, before + W, 3 + b % 7] = NAN            # the row of the second query: all but the first see it
             hit[b, 1:] = True
         check_hits(c.run(csa), want, hit)
+
+
+@pytest.mark.parametrize("B,Nq,H,n_p,own,fp8", SHAPES)
+def test_infinite_keys_reach_every_result_of_their_readers(cuda_lib, B, Nq, H, n_p, own, fp8):
+    """A row with an infinity scores +inf, -inf or NaN by the sign of the head's query there; all its readers' heads,
+    channels and lse are NaN, whichever it is."""
+    csa = cuda_lib
+    c = Case(csa, B, Nq, H, n_p, own, fp8=fp8, n_c=lengths(B, n_p, own), t=positions(B, Nq, n_p, own),
+             seed=B + H)
+    want = c.run(csa)
+    hit = torch.zeros(B, Nq, dtype=torch.bool, device=DEV)
+    for b, i, v in ((0, n_p, INF), (1, n_p + own // 2, -INF), (2, int(c.n_c[2]) - 1, INF), (B - 1, int(c.n_c[B - 1]) - 3, -INF)):
+        c.cache.rope[b, i, 5] = v
+        hit[b] = True
+    (c.win.rope if fp8 else c.win)[3, W - 1, 11] = -INF     # a row that every query of sequence 3 sees
+    hit[3] = True
+    check_hits(c.run(csa), want, hit)
