@@ -638,8 +638,8 @@ static AttnPlan plan_attn(const csa_attn_args* a, int hca) {
 }
 
 // ptrs = false (workspace-size and kernel-count queries): shapes, flags and the page map only; the buffers
-// may not exist yet
-static csa_status validate_attn(const csa_attn_args* a, int hca, bool ptrs = true) {
+// may not exist yet.  most: splits of a query that the caller's merge takes
+static csa_status validate_attn(const csa_attn_args* a, int hca, bool ptrs = true, int most = MERGE_MAX_SPLITS) {
   CSA_REQUIRE(a != nullptr && a->struct_size == sizeof(csa_attn_args));
   CSA_REQUIRE(a->B >= 0 && a->Nq >= 0 && a->H >= 1 && a->ratio >= 1 && a->n_max >= 0 && a->Wn >= 0 && a->window >= 1);
   CSA_SUPPORTED((a->d == 512 && a->d_rope == 64) || (a->d == 128 && a->d_rope == 32));
@@ -660,7 +660,7 @@ static csa_status validate_attn(const csa_attn_args* a, int hca, bool ptrs = tru
   if (a->Wn > 0 && a->win_format == CSA_WIN_FP8) {
     CSA_REQUIRE(a->win_codes && a->win_scales && a->win_rope && a->win_pos0);
     // FP8 window rows are read by the tensor-core path only (d = 512, 16-byte aligned rows)
-    CSA_SUPPORTED(attn_tc_eligible(a, hca, MERGE_MAX_SPLITS));
+    CSA_SUPPORTED(attn_tc_eligible(a, hca, most));
   }
   return CSA_OK;
 }
@@ -858,7 +858,7 @@ static SharedPlan plan_shared(const csa_shared_attn_args* s) {
 
 static csa_status validate_shared(const csa_shared_attn_args* s, bool ptrs) {
   CSA_REQUIRE(s != nullptr && s->struct_size == sizeof(csa_shared_attn_args));
-  const csa_status v = validate_attn(&s->attn, 1, ptrs);
+  const csa_status v = validate_attn(&s->attn, 1, ptrs, 1 << 30);    // (attn_shared_merge_kernel takes any number)
   if (v != CSA_OK) return v;
   CSA_REQUIRE(s->n_prefix >= 0 && s->n_prefix <= s->attn.n_max);
   CSA_REQUIRE(s->attn.softmax_scale >= 0.0f);    // (false for NaN too)
