@@ -844,9 +844,9 @@ static SharedPlan plan_shared(const csa_shared_attn_args* s) {
   const csa_attn_args* a = &s->attn;
   SharedPlan p{};
   const long long own = (long long)a->n_max - s->n_prefix + (attn_has_window(a) ? a->Wn : 0);
-  p.rows = own > 0 && attn_prefix_takes_own(a, s->n_prefix);
+  p.rows = own > 0 && s->n_prefix > 0 && attn_prefix_takes_own(a, s->n_prefix);
   if (own > 0 && !p.rows) attn_tc_plan(a, 1, s->n_prefix, &p.own, &p.tpc);
-  attn_prefix_plan(a, s->n_prefix, p.rows, MERGE_MAX_SPLITS, &p.pairs, &p.pslots);
+  if (s->n_prefix > 0) attn_prefix_plan(a, s->n_prefix, p.rows, MERGE_MAX_SPLITS, &p.pairs, &p.pslots);
   const size_t parts = (size_t)a->B * a->Nq * (p.own + p.pslots) * a->H;
   p.off_scale = align_up(parts * 512 * 2, 256);
   p.off_lse = align_up(p.off_scale + parts * 8 * 4, 256);
@@ -854,6 +854,15 @@ static SharedPlan plan_shared(const csa_shared_attn_args* s) {
   // (their rows, then one mark a row)
   p.total = p.off_rows + (p.rows ? (size_t)a->B * (own * 1024 + align_up((size_t)own, 256)) : 0);
   return p;
+}
+
+// A call without a prefix that is one of hca_dense_attn: its splits fit that one's merge (one query of 129 to 148 tiles
+// has more, and hca_dense_attn's other kernel for it reads bf16 windows only).
+static bool shared_is_dense(const csa_shared_attn_args* s) {
+  if (s->n_prefix > 0) return false;
+  int splits = 0, tpc = 0;
+  attn_tc_plan(&s->attn, 1, 0, &splits, &tpc);
+  return splits <= MERGE_MAX_SPLITS;
 }
 
 static csa_status validate_shared(const csa_shared_attn_args* s, bool ptrs) {
@@ -875,11 +884,11 @@ static csa_status run_shared(const csa_shared_attn_args* s, void* ws, size_t ws_
   const csa_status v = validate_shared(s, true);
   if (v != CSA_OK) return v;
   const csa_attn_args* a = &s->attn;
-  if (s->n_prefix == 0) return run_attn(a, ws, ws_bytes, st, 1);
   const long long rows = (long long)a->B * a->Nq;
   if (rows == 0) return CSA_OK;
+  if (shared_is_dense(s)) return run_attn(a, ws, ws_bytes, st, 1);
   const SharedPlan p = plan_shared(s);
-  CSA_SUPPORTED(p.pairs > 0);
+  CSA_SUPPORTED(s->n_prefix == 0 || p.pairs > 0);
   if (ws_bytes < p.total) return CSA_ERR_WORKSPACE;
   CSA_REQUIRE(ws != nullptr);
   CSA_SUPPORTED(((uintptr_t)ws & 15) == 0);
@@ -891,7 +900,7 @@ static csa_status run_shared(const csa_shared_attn_args* s, void* ws, size_t ws_
   csa_status r = CSA_OK;
   if (p.rows) r = launch_own_rows(a, s->n_prefix, own_rows, st);
   if (p.own > 0) r = launch_attn_tc(a, 1, s->n_prefix, p.own, slots, p.tpc, po, pl, st);
-  if (r == CSA_OK)
+  if (r == CSA_OK && s->n_prefix > 0)
     r = launch_attn_prefix(a, s->prefix_kv, s->n_prefix, own_rows, p.pairs, p.own, p.pslots, slots, po, ps, pl, st);
   if (r != CSA_OK) return r;
   return (slots <= SMERGE_AT_ONCE ? launch_shared_merge<1> : launch_shared_merge<SMERGE_WARPS>)(
@@ -904,9 +913,9 @@ using namespace csa;
 
 extern "C" size_t csa_shared_attn_workspace_size(const csa_shared_attn_args* a) {
   if (validate_shared(a, false) != CSA_OK || (long long)a->attn.B * a->attn.Nq == 0) return 0;
-  if (a->n_prefix == 0) return plan_attn(&a->attn, 1).total;
+  if (shared_is_dense(a)) return plan_attn(&a->attn, 1).total;
   const SharedPlan p = plan_shared(a);
-  return p.pairs > 0 ? p.total : 0;
+  return a->n_prefix == 0 || p.pairs > 0 ? p.total : 0;
 }
 
 extern "C" csa_status hca_shared_attn(const csa_shared_attn_args* a, void* ws, size_t ws_bytes, void* stream) {
