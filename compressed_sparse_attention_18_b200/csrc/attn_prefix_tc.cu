@@ -492,19 +492,23 @@ static void px_own(const csa_attn_args* a, int n_p, int* nseq, int* otiles) {
 
 // Whether the prefix kernel takes the own keys too (as bf16 rows written by own_rows_kernel), or the per-query attention
 // does: by their times.  A tile takes a pair 4.0 us, rows are written at about 4.2 TB/s; the per-query kernels take about
-// 10 us and 7.9 us a wave of tiles of 128 keys.  Measured, here / there: 16 sequences of 64 heads with 64 own entries
-// after 8192 shared ones 32.7 / 44.6 us, 40 of 16 heads with 3000 after 200 96.0 / 111.8; 64 of 64 with 2000 after
-// 1024 112.2 / 107.1, 200 of 4 with 500 after 300 109.4 / 105.2.  Over 24 such shapes the rule's choice costs 1 % on
-// average, 16 % at most (128 of 16 with 500 after 512, 73.3 / 63.2).
+// 10 us and 7.9 us a wave of tiles of 128 keys.  Here every row of the window buffer counts, there the `window` rows of
+// it that a query can see at most.  Measured, here / there: 16 sequences of 64 heads with 64 own entries
+// after 8192 shared ones 32.7 / 44.6 us, 40 of 16 heads with 3000 after 200 94.6 / 111.4; 64 of 64 with 64 after 8192 and
+// 1024 window rows 127 / 86, 1 of 64 heads and 4096 queries with 64 after 8192 and 4223 window rows 5974 / 4303.  Over 21
+// shapes of 1 to 4096 queries and windows of up to 32 times their length the rule's choice costs 1.3 % on average,
+// 13 % at most (128 of 16 heads with 500 after 512: 69.9 / 61.7, the wrong one).
 bool attn_prefix_takes_own(const csa_attn_args* a, int n_p) {
   int nseq, otiles;
   px_own(a, n_p, &nseq, &otiles);
   const double rows = (double)a->B * a->Nq, R = rows * a->H;
-  const double own = (double)a->n_max - n_p + (attn_has_window(a) ? a->Wn : 0);
+  const double ent = (double)a->n_max - n_p;
+  const double own = ent + (attn_has_window(a) ? a->Wn : 0);
+  const double seen = ent + (attn_has_window(a) ? (a->Wn < a->window ? a->Wn : a->window) : 0);
   if (own * a->B > 2147483647.0) return false;
   const double blocks = (double)((long long)(R + PX_ROWS - 1) / PX_ROWS);
   const double t_here = 4.0 * blocks * nseq * otiles / 74 + a->B * own * 1024 / 4.2e6;
-  const double waves = (double)(long long)((rows * (double)(long long)((own + 127) / 128) + 147) / 148);
+  const double waves = (double)(long long)((rows * (double)(long long)((seen + 127) / 128) + 147) / 148);
   return t_here < 10.0 + 7.9 * waves;
 }
 
