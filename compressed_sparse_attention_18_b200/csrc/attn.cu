@@ -846,6 +846,7 @@ static SharedPlan plan_shared(const csa_shared_attn_args* s) {
   const long long own = (long long)a->n_max - s->n_prefix + (attn_has_window(a) ? a->Wn : 0);
   p.rows = own > 0 && s->n_prefix > 0 && attn_prefix_takes_own(a, s->n_prefix);
   if (own > 0 && !p.rows) attn_tc_plan(a, 1, s->n_prefix, &p.own, &p.tpc);
+  // (without a prefix: the per-query attention's partials alone)
   if (s->n_prefix > 0) attn_prefix_plan(a, s->n_prefix, p.rows, MERGE_MAX_SPLITS, &p.pairs, &p.pslots);
   const size_t parts = (size_t)a->B * a->Nq * (p.own + p.pslots) * a->H;
   p.off_scale = align_up(parts * 512 * 2, 256);

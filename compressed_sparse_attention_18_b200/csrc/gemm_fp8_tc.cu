@@ -18,8 +18,10 @@
 // memory and are added in rank order (the same result at every run).
 // Bounds, measured on B200 (replayed graphs, SM clock 1.7 GHz under the power cap): 4096 tokens into two weights of
 // 512 x 4096 23.6 us = 1450 TFLOP/s, 8192 x 4096 x 4096 1690 TFLOP/s.  The same pair kernel without reading the
-// accumulators until the end reaches 1630 / 2000, without the loads as well 1970 / 2300: what is left is the
-// hand-over of two accumulators (all of tensor memory) and the operand traffic.  Few tokens are bound by latency:
+// accumulators until the end reaches 1630 / 2000, without the loads as well 1970 / 2300.  So at 4096 tokens the hand-over
+// of two accumulators (all of tensor memory) costs 11 %, operands from L2 17 %; the larger rest against the rate of the
+// MMAs is that each pair has one tile there, with nothing beside its first loads and its stores, and 10 of 74 have none.
+// Few tokens are bound by latency:
 // 32 tokens into the two weights take 4.5 us, 4 MB of weights at the copy rate 0.65 us.
 // Warp roles (384 threads): warps 0-7 scale and accumulate (4 lane quadrants x 2 column halves), warp 8 TMA, warps
 // 9 and 10 MMA, warp 11 tensor memory.  Every wait is bounded; a wait that gives up records device error 1 and the kernel leaves.

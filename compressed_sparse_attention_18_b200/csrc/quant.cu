@@ -5,9 +5,9 @@
 //   codes 0 (the rule of the FP8 window rows, with 128 channels to a block).  A NaN has no part in amax and
 //   becomes the NaN code; an infinity makes the scale infinite, itself NaN and the block's other codes 0.
 //
-// Bound by HBM: 2 bytes read and 1 written an element (4096 x 4096: 10.9 us, 4.6 TB/s), with the instructions of the
-// quotients close behind (14 an element, 68 % of the issue slots).  A block is kept in registers between its maximum and
-// its codes, so the source is read once.
+// Bound by HBM: 2 bytes read and 1 written an element (4096 x 4096 in rows: 10.0 us, 5.1 TB/s), with the instructions of
+// the quotients close behind (11.8 an element, 60 % of the issue slots).  A block is kept in registers between its
+// maximum and its codes, so the source is read once.
 #include "csa_common.cuh"
 
 namespace csa {

@@ -319,6 +319,8 @@ csa_status csa_index_topk_noalloc(const csa_index_args* args, void* stream);
  *          win_pos0[b] .. win_pos0[b] + Wn - 1 (absent positions are skipped).
  *   One joint softmax with logits softmax_scale * (q_h · K_j) (softmax_scale == 0 -> 1/sqrt(d)).
  *   out = bf16(sum_j p_j V_j); lse = ln sum_j exp(logit_j) (fp32; -inf and out = 0 for no keys).
+ *   A key with a NaN or an infinity makes out and lse of the queries that see it NaN, and of no others (an infinity only
+ *   with d = 512, and there not for one query of more than 128 tiles of 128 keys: single channels elsewhere).
  * Shapes: q/out[B][Nq][H][d] bf16, q_pos[B][Nq] int64, kv_codes[B][n_max][(d-d_rope)/2],
  *         kv_scales[B][n_max][S_pad], kv_rope[B][n_max][d_rope] bf16, n_c[B] int32,
  *         idx[B][Nq][k] int32, win_kv[B][Wn][d] bf16 (may be NULL with Wn = 0), win_pos0[B] int64,
@@ -396,7 +398,8 @@ csa_status csa_quant_fp8(const csa_quant_fp8_args* args, void* stream);
  * CED bullet eq.(1): C and Z are separate projections of the hidden state), E4M3 operands as csa_quant_fp8 writes
  * them (x with block_rows = 1, each W with block_rows = 128):
  *   out[w][m][n] = bf16( sum_kb x_scales[m][kb] W_scales[w][n / 128][kb] sum_{k in block kb} x[m][k] W[w][n][k] )
- * The products of a 128-wide block of K are summed by the tensor cores in fp32, the scaled blocks in fp32 in the
+ * The products of a 128-wide block of K are summed by the tensor cores in fp32, the scaled blocks in fp32 (the two
+ * scales are multiplied first, also in fp32: their product should stay in its range) in the
  * order of kb (split over up to 8 parts of K, added in order, when a launch has few tiles: the result of a shape is
  * the same at every run).  Weights are [N][K] (K contiguous), the transpose of csa_compress's bf16 W_kv / W_g.
  * Shapes: x[M][K], W[w][N][K] u8; x_scales[M][KB], W_scales[w][ceil(N / 128)][KB] fp32, KB = ceil(K / 128);
@@ -459,7 +462,8 @@ csa_status csa_unpack_fp8_window(const csa_unpack_args* args, void* stream);
  *         128 query rows x 256 keys; q, prefix_kv, the cache, the window and the workspace 16-byte aligned (else
  *         CSA_ERR_UNSUPPORTED).
  * Workspace: csa_shared_attn_workspace_size() (partials, and the own keys as bf16 rows).  Results do not depend on what
- * the workspace held.
+ * the workspace held.  Where the own keys are copied, its size and the call's time follow the cache's capacity
+ * (n_max - n_prefix) and Wn, not n_c: keep n_max near the longest sequence.
  * ------------------------------------------------------------------------------------------------ */
 typedef struct csa_shared_attn_args {
   uint32_t struct_size;
